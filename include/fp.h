@@ -52,7 +52,7 @@ extern "C" {
 
 typedef uint64_t fp_elem;
 
-typedef enum { FP_I8 = 0, FP_I32 = 1 } fp_dtype;
+typedef enum { FP_I8 = 0, FP_I32 = 1, FP_F32 = 2, FP_F16 = 3, FP_BF16 = 4 } fp_dtype;
 
 enum {
   FP_OK = 0,
@@ -66,6 +66,7 @@ enum {
 #define FP_MAX_DIN 131071 /* 128^2 * d_in < 2^31 keeps Z exact in int32 (int8 products reach (-128)^2) */
 #define FP_MAX_N 30       /* largest table: 2^30 entries */
 #define FP_MAX_GROUPS 256 /* groups in one grouped witness launch */
+#define FP_MAX_EXPERTS 1024           /* experts in one device sort */
 #define FP_MAX_REQUESTS 4096          /* eq vectors in one multi-request fold */
 #define FP_MAX_FOLD_ROWS (1 << 30)    /* rows of a multi-request fold's matrix */
 #define FP_MAX_RS_LOGN 23             /* Reed-Solomon rows of up to 2^23 elements (codewords 2^24) */
@@ -148,6 +149,49 @@ int fp_moe_plan(const int32_t* route, int32_t T, int32_t n_experts, int32_t* cou
 int fp_gather_rows(const int8_t* X, int64_t ldx, const int32_t* perm, int32_t n_rows, int32_t cols, int8_t* Xg,
                    hipStream_t stream);
 
+/* Tokens sorted by expert on the device (no host plan, several experts a
+ * token). ids (device int32 or int64 by id_bytes 4 or 8, [T, K] dense) holds
+ * each token's experts; slot s = t K + k; an id outside [0, E) is a slot
+ * without an expert (dropped). Writes, all device int32: offsets [E + 1]
+ * (offsets[e]: first sorted row of expert e; offsets[E]: how many slots have
+ * an expert), slots [T K] (sorted row -> slot; ascending within an expert; -1
+ * from row offsets[E] on), tokens [T K] (sorted row -> token; -1 there too)
+ * and rows [T, K] (slot -> sorted row; -1 for a dropped slot). T K < 2^31,
+ * E <= FP_MAX_EXPERTS. ws: fp_moe_sort_workspace bytes (0 for few slots: ws
+ * may be NULL), contents on entry do not matter. */
+int fp_moe_sort(const void* ids, int32_t id_bytes, int32_t T, int32_t K, int32_t E, int32_t* offsets, int32_t* slots,
+                int32_t* tokens, int32_t* rows, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t fp_moe_sort_workspace(int32_t T, int32_t K, int32_t E);
+
+/* Xs[rows[t, k], :] = X[t, :] for every slot with a row in [0, T K): the
+ * tokens' rows in sorted order. Elements of 1, 2 or 4 bytes, d to a row; X
+ * [T, d] (leading dim ldx), Xs [T K, d] (lds). Rows of Xs that no slot has are
+ * left as they were. */
+int fp_moe_permute(int32_t elem_bytes, const void* X, int64_t ldx, int32_t T, int32_t K, int32_t d,
+                   const int32_t* rows, void* Xs, int64_t lds, hipStream_t stream);
+
+/* fp_moe_sort and fp_moe_permute in one call. */
+int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, int32_t d, const void* ids, int32_t id_bytes,
+                    int32_t T, int32_t K, int32_t E, int32_t* offsets, int32_t* slots, int32_t* tokens, int32_t* rows,
+                    void* Xs, int64_t lds, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Y[t, :] = sum_k w[t, k] O[rows[t, k], :] over the slots with a row in
+ * [0, n_rows), k ascending in fp32, rounded once (w: device fp32 [T, K] dense,
+ * NULL: all one, which is the gradient of fp_moe_permute: dX from dXs). O
+ * [n_rows, d] (ldo) and Y [T, d] (ldy) are FP_F32, FP_F16 or FP_BF16. A token
+ * without rows gets zeros. */
+int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n_rows, const int32_t* rows, const float* w,
+                   int32_t T, int32_t K, int32_t d, void* Y, int64_t ldy, hipStream_t stream);
+
+/* The gradients of fp_moe_combine from dY [T, d] (lddy): dO[rows[t, k], :] =
+ * w[t, k] dY[t, :] (rows of dO that no slot has are left as they were; the
+ * rows must be distinct, as fp_moe_sort writes them) and dw[t, k] =
+ * <dY[t, :], O[rows[t, k], :]> (device fp32 [T, K] dense, summed in fp32 in a
+ * fixed order; 0 for a slot without a row). */
+int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int32_t n_rows,
+                            const int32_t* rows, const float* w, int32_t T, int32_t K, int32_t d, void* dO,
+                            int64_t lddo, float* dw, hipStream_t stream);
+
 /* ------------------------------------------------------------------ eq --- */
 /* E[k] = eq(r, k) for k < 2^n (r: n field elements, E: 2^n). n in [0, 30]
  * ("How fast can FlashProve go", §2: the weights of the folded row). */
@@ -203,6 +247,53 @@ int fp_witness_linear_packed_with_sumcheck(const int8_t* X, int64_t ldx, const i
                                            const fp_elem* const* B, const fp_elem* rho, int32_t n,
                                            const fp_elem* r, fp_elem* rounds, fp_elem* finals, fp_elem* claim0,
                                            int32_t n_eq, const fp_eq_desc* eq, hipStream_t stream);
+
+/* ----------------------------------------------------- scaled products --- */
+/* The answer of a quantized layer beside its witness: the integer product with
+ * a scale for each token and each output channel,
+ *   Z[t, o] = sum_k X[t, k] W[o, k]   (exact, the witness's Z)
+ *   Y[t, o] = (float(Z[t, o]) * x_scale[t]) * w_scale[o] + bias[o]
+ * in fp32 (the second product and the bias in one fused multiply-add), rounded
+ * once to Y's type (FP_F32, FP_F16 or FP_BF16). X: int8 [T, d_in] (leading dim
+ * ldx, any alignment; rows that start on 16 bytes with ldx a multiple of 16
+ * and at least ceil(d_in / 16) * 16 are read in whole 16-byte chunks, those of
+ * the last row included, and the bytes past d_in do not count). Wp: the
+ * weights from fp_witness_pack_weights. x_scale [T], w_scale [d_out], bias
+ * [d_out] or NULL: device fp32. Y [T, d_out] (ldy >= d_out); Z int32 (ldz) or
+ * NULL: not stored. d_in <= FP_MAX_DIN. */
+int fp_scaled_matmul(const int8_t* X, int64_t ldx, const float* x_scale, const int8_t* Wp, const float* w_scale,
+                     const float* bias, int32_t T, int32_t d_in, int32_t d_out, fp_dtype y_dt, void* Y, int64_t ldy,
+                     int32_t* Z, int64_t ldz, hipStream_t stream);
+
+/* Row quantization: with a = max_k |X[t, k]|, scale[t] = a / 127 and
+ * Xq[t, k] = rint(X[t, k] * (127 / a)) (fp32, ties to even; |Xq| <= 127). X:
+ * FP_F32, FP_F16 or FP_BF16 [T, cols] (ldx); Xq int8 (ldq >= cols). A row of
+ * zeros has scale 0; a row with an infinity or a NaN has scale NaN and zeros,
+ * so that a product with it is NaN. */
+int fp_quantize_rows(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t cols, int8_t* Xq, int64_t ldq,
+                     float* scale, hipStream_t stream);
+
+/* fp_quantize_rows of X and fp_scaled_matmul of the result: the same Y and Z.
+ * ws: fp_scaled_linear_workspace(T, d_in) bytes, 256-byte aligned (the
+ * quantized rows and their scales), contents on entry do not matter. */
+int fp_scaled_linear(fp_dtype x_dt, const void* X, int64_t ldx, const int8_t* Wp, const float* w_scale,
+                     const float* bias, int32_t T, int32_t d_in, int32_t d_out, fp_dtype y_dt, void* Y, int64_t ldy,
+                     int32_t* Z, int64_t ldz, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t fp_scaled_linear_workspace(int32_t T, int32_t d_in);
+
+/* fp_scaled_matmul for G groups of rows (one per expert) whose bounds only the
+ * device knows: group g owns output rows [offsets[g], offsets[g + 1]) (device
+ * int32 [G + 1], non-decreasing, in [0, n_rows]; fp_moe_sort writes them) and
+ * multiplies by Wp[g] (HOST array of G device pointers, read during the call),
+ * with scales and bias at w_scale[g ld_scale + o] (bias likewise, or NULL).
+ * Output row i is made from row rows[i] of X (device int32 [n_rows], e.g.
+ * fp_moe_sort's tokens; NULL: row i), X having x_rows rows and x_scale as many
+ * entries. Output rows of no group, and rows whose index is outside
+ * [0, x_rows), are left as they were. G <= FP_MAX_GROUPS. */
+int fp_scaled_matmul_grouped(const int8_t* X, int64_t ldx, const float* x_scale, int32_t x_rows, const int32_t* rows,
+                             int32_t n_rows, const int8_t* const* Wp, const float* w_scale, const float* bias,
+                             int64_t ld_scale, const int32_t* offsets, int32_t G, int32_t d_in, int32_t d_out,
+                             fp_dtype y_dt, void* Y, int64_t ldy, int32_t* Z, int64_t ldz, hipStream_t stream);
 
 /* --------------------------------------------------------------- folds --- */
 /* Folded row of an integer matrix ("How fast can FlashProve go", §2: the

@@ -15,7 +15,7 @@ import os
 import torch
 
 P = 0xFFFFFFFF00000001
-FP_I8, FP_I32 = 0, 1
+FP_I8, FP_I32, FP_F32, FP_F16, FP_BF16 = 0, 1, 2, 3, 4
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfp.so")
 EXPORTS = [
@@ -36,6 +36,9 @@ EXPORTS = [
     "fp_witness_grouped_packed", "fp_witness_grouped_packed_workspace",
     "fp_sumcheck_ext_fs_multi", "fp_sumcheck_ext_fs_multi_workspace", "fp_commit_tables", "fp_commit_fold_ext",
     "fp_commit_fold_ext_workspace", "fp_merkle_open", "fp_lookup_tree_pairs", "fp_lookup_counts_field",
+    "fp_quantize_rows", "fp_scaled_matmul", "fp_scaled_linear", "fp_scaled_linear_workspace", "fp_scaled_matmul_grouped",
+    "fp_moe_sort", "fp_moe_sort_workspace", "fp_moe_permute", "fp_moe_dispatch", "fp_moe_combine",
+    "fp_moe_combine_backward",
 ]
 
 _lib = None
@@ -170,6 +173,21 @@ def lib():
             "fp_merkle_open": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp]),
             "fp_lookup_tree_pairs": (ctypes.c_int, [vp, vp, i64, u64, u64, i32, vp, vp, vp]),
             "fp_lookup_counts_field": (ctypes.c_int, [vp, i64, i64, i32, vp, vp]),
+            "fp_quantize_rows": (ctypes.c_int, [i32, vp, i64, i32, i32, vp, i64, vp, vp]),
+            "fp_scaled_matmul": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp]),
+            "fp_scaled_linear": (ctypes.c_int, [i32, vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, sz,
+                                                vp]),
+            "fp_scaled_linear_workspace": (sz, [i32, i32]),
+            "fp_scaled_matmul_grouped": (ctypes.c_int, [vp, i64, vp, i32, vp, i32, vp, vp, vp, i64, vp, i32, i32, i32,
+                                                        i32, vp, i64, vp, i64, vp]),
+            "fp_moe_sort": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "fp_moe_sort_workspace": (sz, [i32, i32, i32]),
+            "fp_moe_permute": (ctypes.c_int, [i32, vp, i64, i32, i32, i32, vp, vp, i64, vp]),
+            "fp_moe_dispatch": (ctypes.c_int, [i32, vp, i64, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp,
+                                               sz, vp]),
+            "fp_moe_combine": (ctypes.c_int, [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp]),
+            "fp_moe_combine_backward": (ctypes.c_int, [i32, vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp,
+                                                       vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -587,6 +605,318 @@ def gather_rows(X, perm_dev, out=None):
     _check(lib().fp_gather_rows(_ptr(X), _ld(X), _ptr(perm_dev), n, cols, _ptr(out), _stream()),
            "fp_gather_rows")
     return out
+
+
+# ---------------------------------------------------------- scaled products --
+_FLOATS = {torch.float32: FP_F32, torch.float16: FP_F16, torch.bfloat16: FP_BF16}
+
+
+def _float_dt(dtype, name: str) -> int:
+    dt = _FLOATS.get(dtype)
+    if dt is None:
+        raise ValueError("%s: dtype %s, expected float32, float16 or bfloat16" % (name, dtype))
+    return dt
+
+
+def _matrix(t, dtype, rows, cols: int, name: str):
+    """Check a row-major device matrix: dtype (None: any), shape (rows None: any) and unit column stride; a matrix that
+    is written (or read) row by row has rows that do not overlap."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols:
+        raise ValueError("%s: shape %s, expected (%s, %d)" % (name, tuple(t.shape), "*" if rows is None else rows, cols))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.numel() and ((cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols)):
+        raise ValueError("%s: rows must be contiguous and must not overlap" % name)
+
+
+def _vector(t, dtype, shape, name: str):
+    """Check a dense device array of this dtype and shape."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: %s %s, expected %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s: must be contiguous" % name)
+
+
+def _here(*named):
+    """Every given tensor is on the current device, where the call's stream and its scratch are."""
+    dev = torch.cuda.current_device()
+    for t in named:
+        if t is not None and not (t.is_cuda and t.get_device() == dev):
+            raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, dev))
+
+
+def _whole_rows(X):
+    """X's rows, when they start on 16 bytes, are read in whole 16-byte chunks: the last row's must be in its storage."""
+    T, d = X.shape
+    ld, up = _ld(X), (d + 15) // 16 * 16
+    if up != d and ld % 16 == 0 and X.data_ptr() % 16 == 0 and ld >= up:
+        end = X.storage_offset() + (T - 1) * ld + up
+        if T and end > X.untyped_storage().nbytes():
+            raise ValueError("X: the last row is read up to column %d, past its storage (copy X, or pad its rows)" % up)
+
+
+def quantize_rows(X, out=None, scale=None):
+    """(Xq, scale): each row of X [T, d] (float32, float16 or bfloat16) as int8 with the scale max|x| / 127, rounded to
+    the nearest (ties to even). Without ``out``, Xq's rows are a multiple of 16 bytes apart, so that the products read
+    them in whole chunks."""
+    if X.dim() != 2:
+        raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
+    T, d = X.shape
+    dt = _float_dt(X.dtype, "X")
+    _matrix(X, None, T, d, "X")
+    if out is None:
+        out = torch.empty((T, (d + 15) // 16 * 16), dtype=torch.int8, device=X.device)[:, :d]
+    else:
+        _matrix(out, torch.int8, T, d, "out")
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=X.device)
+    else:
+        _vector(scale, torch.float32, (T,), "scale")
+    _here(X, out, scale)
+    _check(lib().fp_quantize_rows(dt, X.data_ptr(), _ld(X), T, d, out.data_ptr(), _ld(out), scale.data_ptr(),
+                                  _stream()), "fp_quantize_rows")
+    return out, scale
+
+
+def _product_out(T, d_out, out, dtype, Z, device):
+    if out is None:
+        out = torch.empty((T, d_out), dtype=dtype, device=device)
+    else:
+        _matrix(out, None, T, d_out, "out")
+    dt = _float_dt(out.dtype, "out")
+    if Z is not None:
+        _matrix(Z, torch.int32, T, d_out, "Z")
+    return out, dt, (0 if Z is None else Z.data_ptr()), (d_out if Z is None else _ld(Z))
+
+
+def scaled_matmul(X, x_scale, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=torch.bfloat16, Z=None):
+    """Y[t, o] = x_scale[t] w_scale[o] sum_k X[t, k] W[o, k] + bias[o] for int8 X [T, d_in] and packed weights, in
+    ``out``'s type or ``dtype``; Z (int32 [T, d_out] or None) also receives the integer product, the layer's witness."""
+    _matrix(X, torch.int8, None, Wp.d_in, "X")
+    T, d_out = X.shape[0], Wp.d_out
+    _vector(x_scale, torch.float32, (T,), "x_scale")
+    _vector(w_scale, torch.float32, (d_out,), "w_scale")
+    if bias is not None:
+        _vector(bias, torch.float32, (d_out,), "bias")
+    out, dt, z, ldz = _product_out(T, d_out, out, dtype, Z, X.device)
+    _here(X, x_scale, Wp.data, w_scale, bias, out, Z)
+    _whole_rows(X)
+    _check(lib().fp_scaled_matmul(X.data_ptr(), _ld(X), x_scale.data_ptr(), Wp.data.data_ptr(), w_scale.data_ptr(),
+                                  0 if bias is None else bias.data_ptr(), T, Wp.d_in, d_out, dt, out.data_ptr(),
+                                  _ld(out), z, ldz, _stream()), "fp_scaled_matmul")
+    return out
+
+
+def scaled_linear(X, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=None, Z=None):
+    """scaled_matmul of quantize_rows(X) for X [T, d_in] in float32, float16 or bfloat16; the answer is in ``out``'s
+    type, ``dtype`` or X's."""
+    if X.dim() != 2 or X.shape[1] != Wp.d_in:
+        raise ValueError("X: shape %s, expected (*, %d)" % (tuple(X.shape), Wp.d_in))
+    x_dt = _float_dt(X.dtype, "X")
+    _matrix(X, None, None, Wp.d_in, "X")
+    T, d_out = X.shape[0], Wp.d_out
+    _vector(w_scale, torch.float32, (d_out,), "w_scale")
+    if bias is not None:
+        _vector(bias, torch.float32, (d_out,), "bias")
+    out, dt, z, ldz = _product_out(T, d_out, out, dtype or X.dtype, Z, X.device)
+    _here(X, Wp.data, w_scale, bias, out, Z)
+    nbytes = lib().fp_scaled_linear_workspace(T, Wp.d_in)
+    # from the allocator each time, which keeps scratch of different streams and captured graphs apart
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    _check(lib().fp_scaled_linear(x_dt, X.data_ptr(), _ld(X), Wp.data.data_ptr(), w_scale.data_ptr(),
+                                  0 if bias is None else bias.data_ptr(), T, Wp.d_in, d_out, dt, out.data_ptr(),
+                                  _ld(out), z, ldz, ws.data_ptr(), nbytes, _stream()), "fp_scaled_linear")
+    return out
+
+
+class PackedExperts:
+    """The packed weights of G experts of one shape (pack_experts): ``weights`` holds each one's PackedWeights."""
+
+    def __init__(self, weights):
+        weights = list(weights)
+        if not weights:
+            raise ValueError("no experts")
+        if any((w.d_out, w.d_in) != (weights[0].d_out, weights[0].d_in) for w in weights):
+            raise ValueError("experts of different shapes")
+        self.weights, self.d_out, self.d_in = weights, weights[0].d_out, weights[0].d_in
+        self.device = weights[0].data.device
+        if any(w.data.device != self.device for w in weights):
+            raise ValueError("experts on different devices")
+        self.ptrs = (ctypes.c_void_p * len(weights))(*[w.data.data_ptr() for w in weights])
+
+    def __len__(self):
+        return len(self.weights)
+
+
+def pack_experts(W) -> PackedExperts:
+    """The weights of every expert packed once: W int8 [G, d_out, d_in], or a list of int8 [d_out, d_in]."""
+    return PackedExperts([pack_weights(w) for w in W])
+
+
+def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=None, bias=None, out=None,
+                          dtype=torch.bfloat16, Z=None):
+    """scaled_matmul of each expert with its own rows: output rows [offsets[g], offsets[g + 1]) (int32 [G + 1] on the
+    device, as moe_sort writes them) by expert g with w_scale[g] (float32 [G, d_out]; bias likewise). Output row i is
+    made from X's row rows[i] (int32 on the device, e.g. moe_sort's tokens; None: row i). Rows of no expert are left as
+    they were in ``out`` and Z (a new ``out`` holds whatever its memory held there)."""
+    G, d_out = len(We), We.d_out
+    _matrix(X, torch.int8, None, We.d_in, "X")
+    x_rows = X.shape[0]
+    _vector(x_scale, torch.float32, (x_rows,), "x_scale")
+    _matrix(w_scale, torch.float32, G, d_out, "w_scale")
+    if bias is not None:
+        _matrix(bias, torch.float32, G, d_out, "bias")
+        if _ld(bias) != _ld(w_scale):
+            raise ValueError("bias: row stride %d, w_scale has %d" % (_ld(bias), _ld(w_scale)))
+    _vector(offsets, torch.int32, (G + 1,), "offsets")
+    n = x_rows
+    if rows is not None:
+        n = rows.numel()
+        _vector(rows, torch.int32, (n,), "rows")
+    out, dt, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
+    _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
+    _whole_rows(X)
+    _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), _ld(X), x_scale.data_ptr(), x_rows,
+                                          0 if rows is None else rows.data_ptr(), n, We.ptrs, w_scale.data_ptr(),
+                                          0 if bias is None else bias.data_ptr(), _ld(w_scale), offsets.data_ptr(), G,
+                                          We.d_in, d_out, dt, out.data_ptr(), _ld(out), z, ldz, _stream()),
+           "fp_scaled_matmul_grouped")
+    return out
+
+
+# ------------------------------------------------------- tokens by expert --
+class MoePlan:
+    """The device sort of T tokens with K experts each out of E: offsets int32 [E + 1], slots and tokens int32 [T K]
+    (sorted row -> slot t K + k, and -> t; -1 past the last row with an expert) and rows int32 [T, K] (slot -> sorted
+    row; -1: no expert). Filled by moe_sort or moe_dispatch, on the stream of that call; a program that sorts at every
+    step may keep one."""
+
+    def __init__(self, T: int, K: int, E: int, device=None):
+        if T < 0 or K < 1 or E < 1:
+            raise ValueError("MoePlan: T=%d K=%d E=%d" % (T, K, E))
+        self.T, self.K, self.E = T, K, E
+        n = T * K
+        self.nbytes = lib().fp_moe_sort_workspace(T, K, E)
+        buf = torch.empty(E + 1 + 3 * n + self.nbytes // 4, dtype=torch.int32, device=device or _dev())
+        self.offsets = buf[:E + 1]
+        self.slots, self.tokens = buf[E + 1:E + 1 + n], buf[E + 1 + n:E + 1 + 2 * n]
+        self.rows = buf[E + 1 + 2 * n:E + 1 + 3 * n].view(T, K)
+        self.ws = buf[E + 1 + 3 * n:]
+        self.buf = buf
+
+
+def _sort_args(ids, n_experts: int, plan):
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids: %s %s, expected int32 or int64 (T, K)" % (ids.dtype, tuple(ids.shape)))
+    if not ids.is_contiguous():
+        raise ValueError("ids: must be contiguous")
+    T, K = ids.shape
+    if plan is None:
+        plan = MoePlan(T, K, n_experts, ids.device)
+    elif (plan.T, plan.K, plan.E) != (T, K, n_experts):
+        raise ValueError("plan: for T=%d K=%d E=%d, the call has T=%d K=%d E=%d" % (plan.T, plan.K, plan.E, T, K, n_experts))
+    return plan
+
+
+def moe_sort(ids, n_experts: int, plan: MoePlan | None = None) -> MoePlan:
+    """The slots of ids [T, K] (each token's experts, int32 or int64 on the device) sorted by expert, stably; an id
+    outside [0, n_experts) is a slot without an expert. Nothing is read back by the host (compare moe_plan)."""
+    plan = _sort_args(ids, n_experts, plan)
+    _here(ids, plan.buf)
+    _check(lib().fp_moe_sort(ids.data_ptr(), ids.element_size(), plan.T, plan.K, plan.E, plan.offsets.data_ptr(),
+                             plan.slots.data_ptr(), plan.tokens.data_ptr(), plan.rows.data_ptr(), plan.ws.data_ptr(),
+                             plan.nbytes, _stream()), "fp_moe_sort")
+    return plan
+
+
+def _permute_out(X, plan, out):
+    if X.element_size() not in (1, 2, 4):
+        raise ValueError("X: elements of %d bytes, expected 1, 2 or 4" % X.element_size())
+    if X.dim() != 2:
+        raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
+    d = X.shape[1]
+    _matrix(X, None, plan.T, d, "X")
+    if out is None:
+        return torch.empty((plan.T * plan.K, d), dtype=X.dtype, device=X.device)
+    _matrix(out, X.dtype, plan.T * plan.K, d, "out")
+    return out
+
+
+def moe_permute(X, plan: MoePlan, out=None):
+    """Xs [T K, d]: the tokens' rows X [T, d] in the plan's order. Rows past the last one with an expert are left as
+    they were in ``out`` (a new one holds whatever its memory held there)."""
+    out = _permute_out(X, plan, out)
+    _here(X, plan.buf, out)
+    _check(lib().fp_moe_permute(X.element_size(), X.data_ptr(), _ld(X), plan.T, plan.K, X.shape[1],
+                                plan.rows.data_ptr(), out.data_ptr(), _ld(out), _stream()), "fp_moe_permute")
+    return out
+
+
+def moe_dispatch(X, ids, n_experts: int, plan: MoePlan | None = None, out=None):
+    """(Xs, plan): moe_sort of ids and moe_permute of X in one call."""
+    plan = _sort_args(ids, n_experts, plan)
+    out = _permute_out(X, plan, out)
+    _here(X, ids, plan.buf, out)
+    _check(lib().fp_moe_dispatch(X.element_size(), X.data_ptr(), _ld(X), X.shape[1], ids.data_ptr(),
+                                 ids.element_size(), plan.T, plan.K, plan.E, plan.offsets.data_ptr(),
+                                 plan.slots.data_ptr(), plan.tokens.data_ptr(), plan.rows.data_ptr(), out.data_ptr(),
+                                 _ld(out), plan.ws.data_ptr(), plan.nbytes, _stream()), "fp_moe_dispatch")
+    return out, plan
+
+
+def _combine(O, plan, weights, out, name):
+    if O.dim() != 2:
+        raise ValueError("%s: shape %s, expected two dimensions" % (name, tuple(O.shape)))
+    T, K, d = plan.T, plan.K, O.shape[1]
+    dt = _float_dt(O.dtype, name)
+    _matrix(O, None, T * K, d, name)
+    if weights is not None:
+        _vector(weights, torch.float32, (T, K), "weights")
+    if out is None:
+        out = torch.empty((T, d), dtype=O.dtype, device=O.device)
+    else:
+        _matrix(out, O.dtype, T, d, "out")
+    _here(O, plan.buf, weights, out)
+    _check(lib().fp_moe_combine(dt, O.data_ptr(), _ld(O), T * K, plan.rows.data_ptr(),
+                                0 if weights is None else weights.data_ptr(), T, K, d, out.data_ptr(), _ld(out),
+                                _stream()), "fp_moe_combine")
+    return out
+
+
+def moe_combine(O, plan: MoePlan, weights=None, out=None):
+    """Y [T, d]: each token's rows of O [T K, d] (the experts' outputs in the plan's order) added with its weights
+    (float32 [T, K]; None: all one), in fp32, k ascending."""
+    return _combine(O, plan, weights, out, "O")
+
+
+def moe_dispatch_backward(dXs, plan: MoePlan, out=None):
+    """dX [T, d], the gradient of moe_permute and moe_dispatch: each token's rows of dXs [T K, d] added."""
+    return _combine(dXs, plan, None, out, "dXs")
+
+
+def moe_combine_backward(dY, O, plan: MoePlan, weights, dO=None, dw=None):
+    """(dO [T K, d], dw [T, K]), the gradients of moe_combine. Rows of dO past the last one with an expert are left as
+    they were (a new one holds whatever its memory held there); dw is zero for a slot without an expert."""
+    if O.dim() != 2:
+        raise ValueError("O: shape %s, expected two dimensions" % (tuple(O.shape),))
+    T, K, d = plan.T, plan.K, O.shape[1]
+    dt = _float_dt(O.dtype, "O")
+    _matrix(O, None, T * K, d, "O")
+    _matrix(dY, O.dtype, T, d, "dY")
+    _vector(weights, torch.float32, (T, K), "weights")
+    if dO is None:
+        dO = torch.empty((T * K, d), dtype=O.dtype, device=O.device)
+    else:
+        _matrix(dO, O.dtype, T * K, d, "dO")
+    if dw is None:
+        dw = torch.empty((T, K), dtype=torch.float32, device=O.device)
+    else:
+        _vector(dw, torch.float32, (T, K), "dw")
+    _here(dY, O, plan.buf, weights, dO, dw)
+    _check(lib().fp_moe_combine_backward(dt, dY.data_ptr(), _ld(dY), O.data_ptr(), _ld(O), T * K, plan.rows.data_ptr(),
+                                         weights.data_ptr(), T, K, d, dO.data_ptr(), _ld(dO), dw.data_ptr(), _stream()),
+           "fp_moe_combine_backward")
+    return dO, dw
 
 
 # ----------------------------------------------------------------------- eq --
