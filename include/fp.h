@@ -266,7 +266,8 @@ int fp_scaled_matmul(const int8_t* X, int64_t ldx, const float* x_scale, const i
                      int32_t* Z, int64_t ldz, hipStream_t stream);
 
 /* Row quantization: with a = max_k |X[t, k]|, scale[t] = a / 127 and
- * Xq[t, k] = rint(X[t, k] * (127 / a)) (fp32, ties to even; |Xq| <= 127). X:
+ * Xq[t, k] = rint(X[t, k] * (127 * (1 / a))) (each step in fp32, ties to even;
+ * |Xq| <= 127). X:
  * FP_F32, FP_F16 or FP_BF16 [T, cols] (ldx); Xq int8 (ldq >= cols). A row of
  * zeros has scale 0; a row with an infinity or a NaN has scale NaN and zeros,
  * so that a product with it is NaN. */

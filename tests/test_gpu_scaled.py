@@ -140,7 +140,7 @@ def quantized(x):
     top = np.abs(x).max(axis=1, initial=0).astype(np.float32)
     pre = np.where(top < np.float32(2.0 ** -100), np.float32(2.0 ** 64), np.float32(1)).astype(np.float32)
     with np.errstate(all="ignore"):
-        inv = np.where(top > 0, np.float32(127) / (top * pre), np.float32(0)).astype(np.float32)
+        inv = np.where(top > 0, np.float32(127) * (np.float32(1) / (top * pre)), np.float32(0)).astype(np.float32)
         q = np.rint((x * pre[:, None]).astype(np.float32) * inv[:, None]).astype(np.float32)
         scale = (top / np.float32(127)).astype(np.float32)
     bad = ~np.isfinite(x).all(axis=1)

@@ -20,9 +20,11 @@
 namespace {
 
 using sdev::load_elem;
+using sdev::v4f;
 
 // ---- row quantization ------------------------------------------------------
-// scale = max |x| / 127, q = rint(x * (127 / max |x|)). Below 2^-100 the
+// scale = max |x| / 127, q = rint(x * (127 * (1 / max |x|))), each step rounded
+// to fp32 (q is within 2^-15 of a half step of the value at worst). Below 2^-100 the
 // reciprocal would leave fp32, so such a row is first multiplied by 2^64
 // (exact); a row of zeros gets scale 0 and zeros; a row with an infinity or a
 // NaN gets scale NaN and zeros, so that every product with it is NaN.
@@ -95,7 +97,7 @@ struct ScaledArgs {
   int64_t ldy;
   int32_t* Z;
   int64_t ldz;
-  int32_t wp_rb, wp_kb, tiles_t, tiles_o;
+  int32_t wp_rb, wp_kb, tiles_t, tiles_o, group_o, whole;
   int32_t vecY, vecZ;
   // grouped: row i of the output is row rows[i] (or i) of X; group g owns
   // output rows [offsets[g], offsets[g + 1])
@@ -107,84 +109,352 @@ struct GroupPtrs {
   const int8_t* W[FP_MAX_GROUPS];
 };
 
-template <int NW, int TM, int TN>
-struct SCfg {
-  static constexpr int NT = NW * 64, BO = NW * 32 * TM, BT = 32 * TN, BK = WP_BK, PITCH = BK + 16, CPR = BK / 16;
-  static constexpr int NCB = BT * CPR, CB = (NCB + NT - 1) / NT, KS = BK / 32;
-  static constexpr int LDS_BYTES = 2 * BT * PITCH;
-  static_assert(NCB % NT == 0 || NCB < NT, "X chunks: whole rounds, or fewer chunks than threads");
+struct ScaleTables {
+  float ws[256], bias[256], xs[256];
+  int row[256];
 };
 
-// One tile: NW waves of 32 TM outputs x 32 TN tokens. Weight fragments stream
-// from the packed layout into registers PFW blocks ahead; X passes through
-// two LDS stages, loaded PFX blocks ahead. XV: X's rows are whole 16-byte
-// chunks (else bytes are gathered).
-template <int NW, int TM, int TN, bool GROUPED, bool XV, typename YT>
-__global__ __launch_bounds__(NW * 64) void scaled_kernel(ScaledArgs a, GroupPtrs gp) {
-  using C = SCfg<NW, TM, TN>;
-  constexpr int NT = C::NT, BO = C::BO, BT = C::BT, BK = C::BK, PITCH = C::PITCH, CPR = C::CPR, CB = C::CB, KS = C::KS;
-  constexpr int PFW = 2, PFX = 2;
-  __shared__ __align__(16) int8_t sB[2][BT * PITCH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// ---- large products: two groups of four waves in turn ----------------------
+// A workgroup of eight waves makes a tile of 256 outputs x 64 TN tokens, four
+// waves along the outputs (64 each) and two along the tokens (32 TN each).
+// Each K block of 64 bytes is two phases for a wave, a barrier after each: in
+// the first it reads its X fragments from LDS (and stores X of the stage after);
+// in the second it issues its 4 TN products with the loads of later blocks
+// between them. The two groups of waves
+// (the lower and the upper 128 outputs; one wave of each on every SIMD) run
+// one phase apart, so that one wave's products fill the matrix cores while the
+// other's fragments arrive. The two waves that share weight fragments are in
+// one group, so that the second's loads find the first's in L1. X is staged
+// two blocks (whole 128-byte lines) at a time.
+template <int TN>
+struct PCfg {
+  static constexpr int NT = 512, BO = 256, BT = 64 * TN, BK = WP_BK, XK = 2 * BK, PITCH = XK + 16, NCB = BT * 8, CB = NCB / NT;
+  static constexpr int EP = 68;  // words per token of a wave's 64 outputs in the epilogue
+  static constexpr int LDS_BYTES = 2 * BT * PITCH;
+  static_assert(NCB % NT == 0, "X chunks: whole rounds");
+  static_assert(TN < 4 || LDS_BYTES >= 8 * 32 * EP * 4, "the epilogue's rows fit the widest tile's stages");
+};
+
+// The tile of outputs o_base.. and tokens [t_base, t_lim) (at most 64 TN).
+template <int TN, bool GROUPED, typename YT>
+__device__ __forceinline__ void turns_body(const ScaledArgs& a, const int8_t* W, const float* wsc, const float* bias,
+                                           int o_base, int t_base, int t_lim, int8_t* lds) {
+  using C = PCfg<TN>;
+  constexpr int NT = C::NT, BT = C::BT, BK = C::BK, PITCH = C::PITCH, CB = C::CB, TM = 2, KS = 2;
+  constexpr int PFW = 3, U = 12;  // weight blocks in registers; steps after which slots and stages repeat
+  ScaleTables& tab = *reinterpret_cast<ScaleTables*>(lds + PCfg<4>::LDS_BYTES);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int tile = xcd_tile(blockIdx.x, gridDim.x);
-  const int tt = tile % a.tiles_t, to = tile / a.tiles_t;
-  const int o_base = to * BO, wo0 = wave * 32 * TM;
-  int t_base = tt * BT, t_lim = a.T;
-  const int8_t* W = a.W;
-  const float* wsc = a.ws;
-  const float* bias = a.bias;
-  if constexpr (GROUPED) {
-    const sdev::GroupTile gt = sdev::find_group<BT>(a.offsets, a.G, a.T, tt, lane);
-    if (gt.g < 0) return;  // uniform: every wave finds the same
-    t_base = gt.t_base;
-    t_lim = gt.t_lim;
-    W = gp.W[gt.g];
-    wsc += gt.g * a.ldws;
-    if (bias) bias += gt.g * a.ldws;
-  }
-  // output row -> row of X, -1 where there is none
+  const int group = wave >> 2;
+  const int wo0 = (wave >> 2) * 128 + (wave & 1) * 64, wt0 = ((wave >> 1) & 1) * 32 * TN;
   auto x_row = [&](int t) -> int {
     if (t >= t_lim) return -1;
     if (!GROUPED || !a.rows) return t;
     const int x = a.rows[t];
     return (uint32_t)x < (uint32_t)a.x_rows ? x : -1;
   };
+  // the epilogue's scales and rows, read while the products run (each loaded
+  // where it is used, a tile's epilogue took 15 us)
+  if (tid < 256) {
+    const int o = min(o_base + tid, a.N - 1);
+    tab.ws[tid] = wsc[o];
+    tab.bias[tid] = bias ? bias[o] : 0.f;
+  } else if (tid - 256 < BT) {
+    const int x = x_row(t_base + tid - 256);
+    tab.row[tid - 256] = x;
+    tab.xs[tid - 256] = x >= 0 ? a.xs[x] : 0.f;
+  }
   const int NB = a.wp_kb;
   const int64_t rb_bytes = (int64_t)NB * BK * 32;
   const int8_t* pw[TM];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) pw[i] = W + (int64_t)min((o_base + wo0) / 32 + i, a.wp_rb - 1) * rb_bytes + lane * 16;
+  for (int i = 0; i < TM; ++i) pw[i] = W + (int64_t)min((o_base + wo0) / 32 + i, a.wp_rb - 1) * rb_bytes;  // uniform
   const int8_t* px[CB];
-  int kc[CB], so[CB];
+  int so[CB];
+  const int kc = (tid & 7) * 16;
 #pragma unroll
   for (int c = 0; c < CB; ++c) {
-    const int ch = (tid + c * NT) % C::NCB, row = ch / CPR;
-    kc[c] = (ch % CPR) * 16;
-    px[c] = a.X + (int64_t)max(x_row(t_base + row), 0) * a.ldx;  // rows past the end: row 0, never stored
-    so[c] = row * PITCH + kc[c];
+    const int row = (tid >> 3) + c * (NT / 8);
+    px[c] = a.X + (int64_t)max(x_row(t_base + row), 0) * a.ldx;
+    so[c] = row * PITCH + kc;
   }
-  const bool xstore = C::NCB >= NT || tid < C::NCB;
-  v4i wf[PFW][TM][KS], xr[PFX][CB];
+  v4i wf[PFW][TM][KS], xr[CB], fb[KS][TN];
   auto wload = [&](int slot, int kb) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int q = 0; q < KS; ++q) wf[slot][i][q] = *(const v4i*)(pw[i] + (int64_t)kb * (BK * 32) + 1024 * q);
+      for (int q = 0; q < KS; ++q) wf[slot][i][q] = *(const v4i*)(pw[i] + (int64_t)kb * (BK * 32) + 1024 * q + lane * 16);
   };
-  // chunks past d_in are read from column 0 (they meet zero weights)
-  auto xload = [&](int slot, int kb) {
+  auto xload = [&](int stage) {
+    const int k = stage * C::XK + kc;
 #pragma unroll
-    for (int c = 0; c < CB; ++c) {
-      const int k = kb * BK + kc[c];
+    for (int c = 0; c < CB; ++c) xr[c] = *(const v4i*)(px[c] + (k < a.K ? k : 0));
+  };
+  auto sstore = [&](int8_t* buf) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c) *(v4i*)(buf + so[c]) = xr[c];
+  };
+  v16i acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  auto turn = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (NB > 0) {
+#pragma unroll
+    for (int p = 0; p < PFW - 1; ++p) wload(p, min(p, NB - 1));
+    xload(0);
+    sstore(lds);
+    xload(1);
+    turn();
+    if (group) turn();  // the second group starts a phase later
+    // one K block; the stages of X alternate between the halves of the LDS
+    auto step = [&](auto uc, int st) {
+      constexpr int u = decltype(uc)::value;
+      const int8_t* B = lds + (u / 2 % 2) * (BT * PITCH) + (wt0 + r) * PITCH + (u % 2) * BK + 32 * h;
+#pragma unroll
+      for (int q = 0; q < KS; ++q)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[q][j] = *(const v4i*)(B + 32 * j * PITCH + 16 * q);
+      if constexpr (u % 2 == 0) sstore(lds + (1 - u / 2 % 2) * (BT * PITCH));
+      turn();
+      wload((u + PFW - 1) % PFW, min(st + PFW - 1, NB - 1));
+      if constexpr (u % 2 == 0) xload(st / 2 + 2);
+#pragma unroll
+      for (int q = 0; q < KS; ++q)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u % PFW][i][q], fb[q][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int m = 0; m < TM * TN; ++m) {  // a load between every two products
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+      turn();
+    };
+    int kt = 0;
+    for (; kt + U <= NB; kt += U)
+      [&]<int... I>(std::integer_sequence<int, I...>) { (step(std::integral_constant<int, I>{}, kt + I), ...); }(
+          std::make_integer_sequence<int, U>{});
+    [&]<int... I>(std::integer_sequence<int, I...>) {
+      ((kt + I < NB ? step(std::integral_constant<int, I>{}, kt + I) : void()), ...);
+    }(std::make_integer_sequence<int, U - 1>{});
+    if (!group) turn();  // as many barriers as the second group
+  }
+  // ---- epilogue: each wave's products pass through LDS 32 tokens at a time,
+  // so that 16 lanes store a row's 64 outputs (128 bytes of bf16) together
+  __syncthreads();  // every wave is done with X, and the tables are written
+  int32_t* E = reinterpret_cast<int32_t*>(lds) + wave * 32 * C::EP;
+  const int ol = wo0 + (lane & 15) * 4, o0 = o_base + ol, nv = min(a.N - o0, 4);
+  const v4f w4 = *(const v4f*)&tab.ws[ol], b4 = *(const v4f*)&tab.bias[ol];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)  // lane (token r, h) register 4 g + e: output 8 g + 4 h + e
+        *(v4i*)&E[r * C::EP + 32 * i + 8 * g + 4 * h] =
+            v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+    for (int p = 0; p < 8; ++p) {
+      const int row = 4 * p + (lane >> 4), tl = wt0 + 32 * j + row;
+      const v4i z = *(const v4i*)&E[row * C::EP + (lane & 15) * 4];
+      if (tab.row[tl] < 0 || nv <= 0) continue;
+      const int64_t t = t_base + tl;
+      sdev::store4<YT>(z, tab.xs[tl], w4, b4, nv, (YT*)a.Y + t * a.ldy + o0, a.vecY, a.Z ? a.Z + t * a.ldz + o0 : nullptr,
+                       a.vecZ);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// The dense launch makes `whole` tiles of 256 tokens and then every remaining
+// tile as two of 128: the remainder of tiles over the 256 CUs (a workgroup
+// fills one) would else cost a round of whole tiles. The grouped launch's
+// tiles end with their groups. A tile of few rows takes a narrower body.
+template <bool GROUPED, typename YT>
+__global__ __launch_bounds__(512, 2) void scaled_turns_kernel(ScaledArgs a, GroupPtrs gp) {
+  __shared__ __align__(16) int8_t lds[PCfg<4>::LDS_BYTES + sizeof(ScaleTables)];
+  const int8_t* W = a.W;
+  const float* wsc = a.ws;
+  const float* bias = a.bias;
+  int tile, half = -1, tiles_t = a.tiles_t;
+  const auto place = [&](int& o_base, int& tt) {
+    // group_o weight panels at a time, token tiles outermost: the 32 tiles that
+    // an XCD's CUs make at once share 8 token tiles and 4 panels in its L2
+    const int gsz = a.group_o * tiles_t;
+    const int og = tile / gsz, in = tile - og * gsz;
+    const int go = min(a.group_o, a.tiles_o - og * a.group_o);
+    o_base = (og * a.group_o + in % go) * 256;
+    tt = in / go;
+  };
+  int o_base, tt, t_base, t_lim;
+  if constexpr (GROUPED) {
+    // the grid is for the most tiles the groups can have; the first workgroups make those there are
+    const sdev::GroupTiles<256> tiles(a.offsets, a.G, a.T, threadIdx.x & 63);
+    tiles_t = tiles.total;
+    const int nb = tiles_t * a.tiles_o;
+    if ((int)blockIdx.x >= nb) return;
+    tile = xcd_tile(blockIdx.x, nb);
+    place(o_base, tt);
+    const sdev::GroupTile gt = tiles.find(tt);
+    t_base = gt.t_base;
+    t_lim = gt.t_lim;
+    W = gp.W[gt.g];
+    wsc += gt.g * a.ldws;
+    if (bias) bias += gt.g * a.ldws;
+  } else {
+    if ((int)blockIdx.x < a.whole) {
+      tile = xcd_tile(blockIdx.x, a.whole);
+    } else {
+      const int i = xcd_tile(blockIdx.x - a.whole, gridDim.x - a.whole);
+      tile = a.whole + (i >> 1);
+      half = i & 1;
+    }
+    place(o_base, tt);
+    t_base = tt * 256;
+    t_lim = a.T;
+    if (half >= 0) {
+      t_base += half * 128;
+      t_lim = min(a.T, t_base + 128);
+      if (t_base >= a.T) return;
+    }
+  }
+  const int live = t_lim - t_base;
+  if (live > 128) turns_body<4, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+  else if (live > 64) turns_body<2, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+  else turns_body<1, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+}
+
+// Of these tiles of 256 tokens, how many are made whole.
+int64_t turns_whole(int64_t tiles) {
+  const int64_t rest = tiles % 256;
+  return rest <= 128 ? tiles - rest : tiles;
+}
+
+template <bool GROUPED>
+int launch_turns(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
+  a.tiles_o = (a.N + 255) / 256;
+  a.group_o = 4;
+  const int64_t m = GROUPED ? (a.G < a.T ? a.G : a.T) : 1;
+  a.tiles_t = (int32_t)((a.T + m * 255) / 256);
+  int64_t blocks = (int64_t)a.tiles_t * a.tiles_o;
+  a.whole = 0;
+  if (!GROUPED) {
+    a.whole = (int32_t)turns_whole(blocks);
+    blocks += blocks - a.whole;
+  }
+  if (blocks * 512 > 0x7FFFFFFF) return fpi::fail(FP_ESHAPE, "%s: %lld tiles in one launch", fn, (long long)blocks);
+  const dim3 grid((unsigned)blocks), block(512);
+  if (y_dt == FP_F32) scaled_turns_kernel<GROUPED, float><<<grid, block, 0, st>>>(a, gp);
+  else if (y_dt == FP_F16) scaled_turns_kernel<GROUPED, __half><<<grid, block, 0, st>>>(a, gp);
+  else scaled_turns_kernel<GROUPED, __hip_bfloat16><<<grid, block, 0, st>>>(a, gp);
+  const int rc = fpi::check_launch("scaled_turns_kernel");
+  return rc ? rc : fpi::ok();
+}
+
+// ---- few tokens or small products: the K range split over a workgroup -------
+// A tile is 32 TM outputs x 8 XR tokens. The NW waves of its workgroup take units
+// of 128 bytes of K in turn (unit w, w + NW, ...), each into accumulators of
+// its own. Weight fragments go straight into registers; X is read as whole
+// lines (8 rows of 128 bytes a load) and turned into fragments through LDS that
+// only the wave itself uses, so the loop has no barrier. (Fragments of X read
+// from memory touch 32 rows a load: 38 us against 19 us for 64 tokens, K =
+// 14336, 4096 outputs.) The waves' sums meet in LDS (integers: any order gives
+// the same), 32 tokens at a time, and a thread finishes one output of each.
+template <int NW, int TM, int XR, int PF, bool GROUPED, bool XV, typename YT>
+__global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, GroupPtrs gp) {
+  constexpr int NT = NW * 64, TN = (XR + 3) / 4, BT = 8 * XR, BK = WP_BK, UK = 2 * BK, PX = XR <= 4 ? PF : 1;
+  constexpr int XP = UK + 16;  // bytes per token of a wave's X
+  constexpr int RP = 36;       // words per token of a wave's sums (both: 16-byte rows in distinct banks)
+  static_assert(32 * XP == 32 * RP * 4, "a wave's sums take the space of 32 tokens");
+  __shared__ __align__(16) int8_t lds[NW * 32 * TN * XP];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  int to, t_base, t_lim;
+  const int8_t* W = a.W;
+  const float* wsc = a.ws;
+  const float* bias = a.bias;
+  if constexpr (GROUPED) {
+    const sdev::GroupTiles<BT> tiles(a.offsets, a.G, a.T, lane);
+    const int nb = tiles.total * a.tiles_o;
+    if ((int)blockIdx.x >= nb) return;
+    const int tile = xcd_tile(blockIdx.x, nb);
+    const sdev::GroupTile gt = tiles.find(tile % tiles.total);
+    to = tile / tiles.total;
+    t_base = gt.t_base;
+    t_lim = gt.t_lim;
+    W = gp.W[gt.g];
+    wsc += gt.g * a.ldws;
+    if (bias) bias += gt.g * a.ldws;
+  } else {
+    const int tile = xcd_tile(blockIdx.x, gridDim.x);
+    to = tile / a.tiles_t;
+    t_base = (tile % a.tiles_t) * BT;
+    t_lim = a.T;
+  }
+  auto x_row = [&](int t) -> int {
+    if (t >= t_lim) return -1;
+    if (!GROUPED || !a.rows) return t;
+    const int x = a.rows[t];
+    return (uint32_t)x < (uint32_t)a.x_rows ? x : -1;
+  };
+  const int NB = a.wp_kb, NU = (NB + 1) / 2;
+  const int8_t* pw[TM];  // uniform
+#pragma unroll
+  for (int i = 0; i < TM; ++i) pw[i] = W + (int64_t)min(to * TM + i, a.wp_rb - 1) * NB * (BK * 32);
+  const int8_t* px[XR];
+  // the epilogue's scales, read before the products: a thread finishes one
+  // output of every 32 in every (NT / 32)-th token
+  constexpr int TP = NT / 32, MP = (32 + TP - 1) / TP;
+  float ew[TM], eb[TM], exs[TN][MP];
+  bool elive[TN][MP];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int o = min((to * TM + i) * 32 + (tid & 31), a.N - 1);
+    ew[i] = wsc[o];
+    eb[i] = bias ? bias[o] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int m = 0; m < MP; ++m) {
+      const int tl = (tid >> 5) + m * TP, x = 32 * j + tl < BT ? x_row(t_base + 32 * j + tl) : -1;
+      elive[j][m] = x >= 0;
+      exs[j][m] = x >= 0 ? a.xs[x] : 0.f;
+    }
+  const int kc = (lane & 7) * 16;
+#pragma unroll
+  for (int c = 0; c < XR; ++c) px[c] = a.X + (int64_t)max(x_row(t_base + 8 * c + (lane >> 3)), 0) * a.ldx;
+  int8_t* xw = lds + wave * (32 * TN * XP);
+  int8_t* xs = xw + (lane >> 3) * XP + kc;      // stores: row lane / 8 of 8, chunk lane % 8
+  const int8_t* xf = xw + r * XP + 32 * h;      // fragments
+  v4i wf[PF][TM][4], xr[PX][XR];
+  auto wload = [&](int slot, int u) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        wf[slot][i][q] =
+            *(const v4i*)(pw[i] + (int64_t)min(2 * u + q / 2, NB - 1) * (BK * 32) + 1024 * (q % 2) + lane * 16);
+  };
+  auto xload = [&](int slot, int u) {
+    const int k = u * UK + kc;
+#pragma unroll
+    for (int c = 0; c < XR; ++c) {
       if constexpr (XV) xr[slot][c] = *(const v4i*)(px[c] + (k < a.K ? k : 0));
       else xr[slot][c] = load16(px[c], k, a.K, false);
-    }
-  };
-  auto sstore = [&](int slot, int buf) {
-    if (xstore) {
-#pragma unroll
-      for (int c = 0; c < CB; ++c) *(v4i*)&sB[buf][so[c]] = xr[slot][c];
     }
   };
   v16i acc[TM][TN];
@@ -194,85 +464,127 @@ __global__ __launch_bounds__(NW * 64) void scaled_kernel(ScaledArgs a, GroupPtrs
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  if (NB > 0) {  // d_in = 0: every product is 0
+  if (wave < NU) {
+    const int last = wave + (NU - 1 - wave) / NW * NW;  // this wave's last unit
 #pragma unroll
-    for (int p = 0; p < PFW; ++p) wload(p, min(p, NB - 1));
-#pragma unroll
-    for (int p = 0; p < PFX; ++p) xload(p, min(p, NB - 1));
-    sstore(0, 0);
-    xload(0, min(PFX, NB - 1));
-    __syncthreads();
-    auto step = [&](auto uc, int st) {
-      constexpr int u = decltype(uc)::value;
-      const int8_t* B = &sB[u % 2][r * PITCH + 32 * h];
-#pragma unroll
-      for (int q = 0; q < KS; ++q) {
-        v4i fb[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[j] = *(const v4i*)(B + 32 * j * PITCH + 16 * q);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u % PFW][i][q], fb[j], acc[i][j], 0, 0, 0);
-      }
-      wload(u % PFW, min(st + PFW, NB - 1));
-      sstore((u + 1) % PFX, (u + 1) % 2);
-      xload((u + 1) % PFX, min(st + 1 + PFX, NB - 1));
-      __syncthreads();
-    };
-    constexpr int U = 2;
-    int kt = 0;
-    for (; kt + U <= NB; kt += U) {
-      step(std::integral_constant<int, 0>{}, kt);
-      step(std::integral_constant<int, 1>{}, kt + 1);
+    for (int p = 0; p < PF; ++p) {
+      if (p < PX) xload(p, min(wave + p * NW, last));
+      wload(p, min(wave + p * NW, last));
     }
-    if (kt < NB) step(std::integral_constant<int, 0>{}, kt);
+    for (int u0 = wave; u0 <= last; u0 += PF * NW) {
+#pragma unroll
+      for (int p = 0; p < PF; ++p) {
+        const int u = u0 + p * NW;
+        if (u <= last) {  // uniform
+#pragma unroll
+          for (int c = 0; c < XR; ++c) *(v4i*)(xs + 8 * c * XP) = xr[p % PX][c];
+        }
+        xload(p % PX, min(u + PX * NW, last));
+        if (u <= last) {
+          const bool two = 2 * u + 1 < NB;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q >= 2 && !two) break;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+              const v4i x = *(const v4i*)(xf + 32 * j * XP + BK * (q / 2) + 16 * (q % 2));
+#pragma unroll
+              for (int i = 0; i < TM; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[p][i][q], x, acc[i][j], 0, 0, 0);
+            }
+          }
+        }
+        wload(p, min(u + PF * NW, last));
+      }
+    }
   }
-  // epilogue: a lane holds 16 consecutive outputs of one token
+  // lane (token r, h) register 4 g + e: output 8 g + 4 h + e
+  int32_t* red = reinterpret_cast<int32_t*>(lds);
+  const int live = min(t_lim - t_base, BT);
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
-    const int t = t_base + 32 * j + r;
-    const int xrow = x_row(t);
-    const float xsc = xrow >= 0 ? a.xs[xrow] : 0.f;
+    if (32 * j >= live) break;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      int32_t z[16];
-      fragment_outputs(acc[i][j], z);
-      const int o0 = o_base + wo0 + 32 * i + 16 * h;
-      if (xrow < 0 || o0 >= a.N) continue;
-      sdev::store16<YT>(z, xsc, wsc, bias, o0, a.N, (YT*)a.Y + (int64_t)t * a.ldy, a.vecY,
-                        a.Z ? a.Z + (int64_t)t * a.ldz : nullptr, a.vecZ);
+      __syncthreads();  // every wave is done with X, or with the sums of the last block
+      if (32 * j + r < live) {
+        int32_t* dst = red + (wave * 32 + r) * RP + 4 * h;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(v4i*)(dst + 8 * g) =
+              v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+      }
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < MP; ++m) {
+        const int tl = (tid >> 5) + m * TP, o = (to * TM + i) * 32 + (tid & 31);
+        if (!elive[j][m] || o >= a.N) continue;
+        int32_t z = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) z += red[(w * 32 + tl) * RP + (tid & 31)];
+        const int64_t t = t_base + 32 * j + tl;
+        sdev::store_elem((YT*)a.Y + t * a.ldy + o, __builtin_fmaf((float)z * exs[j][m], ew[i], eb[i]));
+        if (a.Z) a.Z[t * a.ldz + o] = z;
+      }
     }
   }
 }
 
-template <int NW, int TM, int TN, bool GROUPED, bool XV>
-int launch_tile(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
-  using C = SCfg<NW, TM, TN>;
-  a.tiles_o = (a.N + C::BO - 1) / C::BO;
-  if (GROUPED) {
-    // sum over the groups of ceil(rows / BT) <= (T + groups with rows * (BT - 1)) / BT
-    const int64_t m = a.G < a.T ? a.G : a.T;
-    a.tiles_t = (int32_t)((a.T + m * (C::BT - 1)) / C::BT);
-  } else {
-    a.tiles_t = (a.T + C::BT - 1) / C::BT;
-  }
+template <int NW, int TM, int XR, int PF, bool GROUPED, bool XV>
+int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
+  constexpr int BT = 8 * XR, NT = NW * 64;
+  a.tiles_o = (a.wp_rb + TM - 1) / TM;
+  const int64_t m = GROUPED ? (a.G < a.T ? a.G : a.T) : 1;
+  a.tiles_t = (int32_t)((a.T + m * (BT - 1)) / BT);
   const int64_t blocks = (int64_t)a.tiles_t * a.tiles_o;
-  if (blocks * C::NT > 0x7FFFFFFF) return fpi::fail(FP_ESHAPE, "%s: %lld tiles in one launch", fn, (long long)blocks);
-  const dim3 grid((unsigned)blocks), block(C::NT);
-  if (y_dt == FP_F32) scaled_kernel<NW, TM, TN, GROUPED, XV, float><<<grid, block, 0, st>>>(a, gp);
-  else if (y_dt == FP_F16) scaled_kernel<NW, TM, TN, GROUPED, XV, __half><<<grid, block, 0, st>>>(a, gp);
-  else scaled_kernel<NW, TM, TN, GROUPED, XV, __hip_bfloat16><<<grid, block, 0, st>>>(a, gp);
-  const int rc = fpi::check_launch("scaled_kernel");
+  if (blocks * NT > 0x7FFFFFFF) return fpi::fail(FP_ESHAPE, "%s: %lld tiles in one launch", fn, (long long)blocks);
+  const dim3 grid((unsigned)blocks), block(NT);
+  if (y_dt == FP_F32) scaled_rows_kernel<NW, TM, XR, PF, GROUPED, XV, float><<<grid, block, 0, st>>>(a, gp);
+  else if (y_dt == FP_F16) scaled_rows_kernel<NW, TM, XR, PF, GROUPED, XV, __half><<<grid, block, 0, st>>>(a, gp);
+  else scaled_rows_kernel<NW, TM, XR, PF, GROUPED, XV, __hip_bfloat16><<<grid, block, 0, st>>>(a, gp);
+  const int rc = fpi::check_launch("scaled_rows_kernel");
   return rc ? rc : fpi::ok();
 }
 
+// Which kernel and tile (measured in a graph of calls, weights of three layers
+// in turn; a "block" is 64 bytes of K):
+//  - up to 8 rows: 32 outputs x 8 rows (T = 1, 4096 -> 14336: 10.5 us; with
+//    tiles of 32 rows 11.0, of 64 x 64 11.8, the turns kernel 23);
+//  - else the row kernel's largest tile that gives most CUs a workgroup: 64 x 64
+//    (T = 200, 4096 -> 4096: 11.3 us, 32 x 32 15.0), 64 x 32 (T = 128, 14336 ->
+//    4096: 19.3 us, 64 x 64 23.8, 32 x 32 23.3), 32 x 32 (T = 64, 14336 -> 4096:
+//    14.2 us, 64 x 32 18.2, 64 x 64 23.6);
+//  - or the turns kernel where its rounds of tiles cost less: 0.86 us a block
+//    and round of 256-token tiles, 0.5 for the last of 128-token tiles, against
+//    0.115 us a block and 256 tiles of 64 x 64 (T = 512, 4096 -> 14336: 36 us,
+//    64 x 64 53; T = 1000, 2048 -> 2048: 19 us, 64 x 64 13.5).
+// Groups: by the rows a group has on average, more than two take the turns
+// kernel (2048 rows in 128 groups, 5120 -> 8192: 0.92 ms, 64 x 64 1.04, 32 x 32
+// 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.7 us, 18.8, 25.3), fewer the
+// 8-row tiles (16 rows in 16 groups, 4096 -> 14336: 114 us; turns 133).
+// Rows of X that are not whole 16-byte chunks are gathered a byte at a time in
+// 8-row or 64 x 64 tiles.
 template <bool GROUPED, bool XV>
 int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
-  const int64_t per = GROUPED ? a.T / (a.G < a.T ? a.G : a.T) : a.T;  // rows, or a group's rows on average
-  if (per <= 32) return launch_tile<4, 2, 1, GROUPED, XV>(fn, a, gp, y_dt, st);
-  return launch_tile<4, 2, 4, GROUPED, XV>(fn, a, gp, y_dt, st);
+  if constexpr (GROUPED) {
+    const int64_t per = a.T / (a.G < a.T ? a.G : a.T);
+    if (per <= 2) return launch_rows<8, 1, 1, 2, true, XV>(fn, a, gp, y_dt, st);
+    if constexpr (XV) return launch_turns<true>(fn, a, gp, y_dt, st);
+    else return launch_rows<4, 2, 8, 2, true, XV>(fn, a, gp, y_dt, st);
+  } else {
+    if (a.T <= 8) return launch_rows<8, 1, 1, 2, false, XV>(fn, a, gp, y_dt, st);
+    if constexpr (XV) {
+      const int64_t t32 = (a.T + 31) / 32, t64 = (a.T + 63) / 64, o64 = (a.N + 63) / 64;
+      const int64_t tiles = (int64_t)((a.N + 255) / 256) * ((a.T + 255) / 256), whole = turns_whole(tiles);
+      const double turns = 4 + a.wp_kb * (0.86 * (double)((whole + 255) / 256) + (tiles > whole ? 0.5 : 0.0));
+      const double rows = 3 + a.wp_kb * 0.115 * (double)((o64 * t64 + 255) / 256);
+      constexpr int64_t FILL = 192;  // workgroups that occupy most of the CUs
+      if (o64 * t64 >= FILL && turns < rows) return launch_turns<false>(fn, a, gp, y_dt, st);
+      if (o64 * t64 < FILL && o64 * t32 >= FILL) return launch_rows<8, 2, 4, 2, false, true>(fn, a, gp, y_dt, st);
+      if (o64 * t64 < FILL) return launch_rows<8, 1, 4, 2, false, true>(fn, a, gp, y_dt, st);
+    }
+    return launch_rows<4, 2, 8, 2, false, XV>(fn, a, gp, y_dt, st);
+  }
 }
 
 int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }

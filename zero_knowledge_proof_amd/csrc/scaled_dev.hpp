@@ -10,6 +10,8 @@
 namespace sdev {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
 // bf16 bits of a float, rounded to nearest even (NaN stays a quiet NaN).
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
@@ -89,7 +91,7 @@ __device__ __forceinline__ RowScale row_scale(float top) {
   if (!(top < __builtin_inff())) return RowScale{__builtin_nanf(""), 0.f, 0.f};
   s.scale = top / 127.0f;
   s.pre = top < 0x1p-100f ? 0x1p64f : 1.0f;
-  s.inv = top > 0.f ? 127.0f / (top * s.pre) : 0.f;
+  s.inv = top > 0.f ? 127.0f * (1.0f / (top * s.pre)) : 0.f;
   return s;
 }
 __device__ __forceinline__ int quantize(float x, const RowScale& s) {
@@ -98,98 +100,92 @@ __device__ __forceinline__ int quantize(float x, const RowScale& s) {
   return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// 16 consecutive outputs o0.. of one row: scaled, biased, rounded and stored
-// (yrow, zrow: the row's starts; zrow NULL: Z is not kept).
+// nv (1 to 4) consecutive outputs of one row at y (and z, unless NULL).
 template <typename YT>
-__device__ __forceinline__ void store16(const int32_t (&z)[16], float xs, const float* ws, const float* bias, int o0,
-                                        int N, YT* yrow, bool vecY, int32_t* zrow, bool vecZ) {
-  const bool whole = o0 + 16 <= N;
-  uint32_t b[16];
+__device__ __forceinline__ void store4(const v4i& z, float xs, const v4f& ws, const v4f& bias, int nv, YT* y, bool vecY,
+                                       int32_t* zp, bool vecZ) {
+  uint32_t b[4];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int o = whole ? o0 + q : min(o0 + q, N - 1);
-    b[q] = Out<YT>::bits(__builtin_fmaf((float)z[q] * xs, ws[o], bias ? bias[o] : 0.f));
-  }
-  if (whole && vecY) {
-    if constexpr (sizeof(YT) == 4) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(v4i*)(yrow + o0 + 4 * q) = v4i{(int)b[4 * q], (int)b[4 * q + 1], (int)b[4 * q + 2], (int)b[4 * q + 3]};
-    } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *(v4i*)(yrow + o0 + 8 * q) =
-            v4i{(int)(b[8 * q] | b[8 * q + 1] << 16), (int)(b[8 * q + 2] | b[8 * q + 3] << 16),
-                (int)(b[8 * q + 4] | b[8 * q + 5] << 16), (int)(b[8 * q + 6] | b[8 * q + 7] << 16)};
-    }
+  for (int q = 0; q < 4; ++q) b[q] = Out<YT>::bits(__builtin_fmaf((float)z[q] * xs, ws[q], bias[q]));
+  if (nv == 4 && vecY) {
+    if constexpr (sizeof(YT) == 4) *(v4i*)y = v4i{(int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+    else *(v2i*)y = v2i{(int)(b[0] | b[1] << 16), (int)(b[2] | b[3] << 16)};
   } else {
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (o0 + q < N) {
-        if constexpr (sizeof(YT) == 4) *(uint32_t*)(yrow + o0 + q) = b[q];
-        else *(unsigned short*)(yrow + o0 + q) = (unsigned short)b[q];
+    for (int q = 0; q < 4; ++q)
+      if (q < nv) {
+        if constexpr (sizeof(YT) == 4) *(uint32_t*)(y + q) = b[q];
+        else *(unsigned short*)(y + q) = (unsigned short)b[q];
       }
   }
-  if (zrow) {
-    if (whole && vecZ) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(v4i*)(zrow + o0 + 4 * q) = v4i{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+  if (zp) {
+    if (nv == 4 && vecZ) {
+      *(v4i*)zp = z;
     } else {
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (o0 + q < N) zrow[o0 + q] = z[q];
+      for (int q = 0; q < 4; ++q)
+        if (q < nv) zp[q] = z[q];
     }
   }
 }
 
-// Group and rows of token tile tt when group g owns rows [off[g], off[g + 1])
-// and is cut into tiles of BT rows, tiles numbered group after group. Every
-// lane of a wave takes part (each holds consecutive groups; a scan over the
-// lanes numbers their tiles) and gets the same answer; g = -1 past the last
-// tile. Offsets are taken into [0, n]; a group whose end is not after its
-// start is empty.
+// Token tiles of BT rows of groups whose bounds only the device knows: group g
+// owns rows [off[g], off[g + 1]), tiles numbered group after group. Every lane
+// of a wave takes part (each holds consecutive groups; a scan over the lanes
+// numbers their tiles) and gets the same answers. Offsets are taken into
+// [0, n]; a group whose end is not after its start is empty.
 struct GroupTile {
   int g, t_base, t_lim;
 };
 template <int BT>
-__device__ __forceinline__ GroupTile find_group(const int32_t* off, int G, int n, int tt, int lane) {
-  const int per = (G + 63) >> 6, g0 = lane * per;
-  auto at = [&](int g) { return min(max(off[min(g, G)], 0), n); };
-  int mine = 0, a = at(g0);
-  for (int j = 0; j < per; ++j) {
-    const int b = at(g0 + j + 1);
-    if (g0 + j < G && b > a) mine += (b - a + BT - 1) / BT;
-    a = b;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
-  }
-  const int excl = incl - mine;
-  int g = -1, tb = 0, tl = 0;
-  if (tt >= excl && tt < incl) {
-    int left = tt - excl;
-    a = at(g0);
+struct GroupTiles {
+  const int32_t* off;
+  int G, n, per, g0, mine, excl;
+  int total;  // token tiles in all
+
+  __device__ __forceinline__ int at(int g) const { return min(max(off[min(g, G)], 0), n); }
+
+  __device__ __forceinline__ GroupTiles(const int32_t* off_, int G_, int n_, int lane) : off(off_), G(G_), n(n_) {
+    per = (G + 63) >> 6;
+    g0 = lane * per;
+    mine = 0;
+    int a = at(g0);
     for (int j = 0; j < per; ++j) {
       const int b = at(g0 + j + 1);
-      const int nt = (g0 + j < G && b > a) ? (b - a + BT - 1) / BT : 0;
-      if (left >= 0 && left < nt) {
-        g = g0 + j;
-        tb = a + left * BT;
-        tl = b;
-      }
-      left -= nt;
+      if (g0 + j < G && b > a) mine += (b - a + BT - 1) / BT;
       a = b;
     }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += v;
+    }
+    excl = incl - mine;
+    total = __builtin_amdgcn_readlane(incl, 63);
   }
-  const uint64_t m = __ballot(g >= 0);
-  if (!m) return GroupTile{-1, 0, 0};
-  const int src = __builtin_ctzll(m);
-  return GroupTile{__builtin_amdgcn_readlane(g, src), __builtin_amdgcn_readlane(tb, src),
-                   __builtin_amdgcn_readlane(tl, src)};
-}
+
+  // Tile tt < total: its group and rows.
+  __device__ __forceinline__ GroupTile find(int tt) const {
+    int g = -1, tb = 0, tl = 0;
+    if (tt >= excl && tt < excl + mine) {
+      int left = tt - excl, a = at(g0);
+      for (int j = 0; j < per; ++j) {
+        const int b = at(g0 + j + 1);
+        const int nt = (g0 + j < G && b > a) ? (b - a + BT - 1) / BT : 0;
+        if (left >= 0 && left < nt) {
+          g = g0 + j;
+          tb = a + left * BT;
+          tl = b;
+        }
+        left -= nt;
+        a = b;
+      }
+    }
+    const int src = __builtin_ctzll(__ballot(g >= 0));
+    return GroupTile{__builtin_amdgcn_readlane(g, src), __builtin_amdgcn_readlane(tb, src),
+                     __builtin_amdgcn_readlane(tl, src)};
+  }
+};
 
 }  // namespace sdev
