@@ -9,7 +9,9 @@
 //   gradients dX[t] = sum_k dXs[rows[t, k]]
 //             dO[rows[t, k]] = w[t, k] dY[t],  dw[t, k] = <dY[t], O[rows[t, k]]>
 // All but the sort are bound by the rows they move: each is read and written
-// once, a token's row by one workgroup for all its choices.
+// once, a piece of a token's row (a 16-byte load a lane, at whatever address the
+// row has) by one workgroup for all of the token's choices, whose rows are all
+// asked for before the first arrives.
 #include "common.hpp"
 #include "scaled_dev.hpp"
 
@@ -21,6 +23,7 @@ constexpr int SORT_NT = 1024, SORT_NW = SORT_NT / 64;
 constexpr int MAXB = FP_MAX_EXPERTS + 1;  // buckets: the experts, and the slots without one
 constexpr int SORT_ONE = 8 * SORT_NT;     // slots that one workgroup sorts alone
 constexpr int SORT_BLOCKS = 256;          // workgroups of a larger sort, at most
+constexpr int SORT_FUSED = 2048;          // slots up to which the gather ranks its own
 
 struct SortArgs {
   const void* ids;
@@ -45,43 +48,21 @@ __global__ __launch_bounds__(SORT_NT) void sort_hist_kernel(SortArgs a) {
   const int B = a.E + 1;
   for (int e = threadIdx.x; e < B; e += SORT_NT) h[e] = 0;
   __syncthreads();
-  const int lo = blockIdx.x * a.per, hi = min(lo + a.per, a.N);
-  for (int s = lo + threadIdx.x; s < hi; s += SORT_NT) atomicAdd(&h[bucket(a, s)], 1);
+  const int64_t lo = (int64_t)blockIdx.x * a.per, hi = min(lo + a.per, (int64_t)a.N);
+  for (int64_t s = lo + threadIdx.x; s < hi; s += SORT_NT) atomicAdd(&h[bucket(a, (int)s)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < B; e += SORT_NT) a.hist[(int64_t)blockIdx.x * B + e] = h[e];
 }
 
-// Workgroup b places its range: the first row of each bucket from the counts
-// of all ranges (its own alone when there is one), then a round of SORT_NT
-// slots at a time, each lane's rank among its wave's lanes of the same bucket
-// by ballots over the bucket's bits, the waves' counts added in order.
-__global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
-  __shared__ int base[MAXB];
-  __shared__ uint16_t cnt[SORT_NW][MAXB + 1];
-  __shared__ int wsum[SORT_NW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = a.E + 1, b = blockIdx.x;
-  const int lo = b * a.per, hi = min(lo + a.per, a.N);
-  int before[2] = {0, 0}, total[2] = {0, 0};
-  if (a.nblk == 1) {
-    for (int e = tid; e < B; e += SORT_NT) base[e] = 0;
-    __syncthreads();
-    for (int s = tid; s < a.N; s += SORT_NT) atomicAdd(&base[bucket(a, s)], 1);
-    __syncthreads();
+// first[e] = how many of the counts tot[0 .. B) come before e, by the whole
+// workgroup of NT threads (two buckets to a thread).
+template <int NT>
+__device__ __forceinline__ void scan_buckets(const int* tot, int B, int* wsum, int (&first)[2]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int t[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (2 * tid + j < B) total[j] = base[2 * tid + j];
-  } else {
-    for (int q = 0; q < a.nblk; ++q)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (2 * tid + j < B) {
-          const int c = a.hist[(int64_t)q * B + 2 * tid + j];
-          total[j] += c;
-          before[j] += q < b ? c : 0;
-        }
-  }
-  // exclusive scan over the buckets, two to a thread
-  int incl = total[0] + total[1];
+  for (int j = 0; j < 2; ++j) t[j] = 2 * tid + j < B ? tot[2 * tid + j] : 0;
+  int incl = t[0] + t[1];
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(incl, d, 64);
@@ -89,24 +70,64 @@ __global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
   }
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
-  int excl = incl - total[0] - total[1];
+  int excl = incl - t[0] - t[1];
   for (int w = 0; w < wave; ++w) excl += wsum[w];
+  first[0] = excl;
+  first[1] = excl + t[0];
+}
+
+// Workgroup b places its range: the first row of each bucket from the counts
+// of all ranges (its own alone when there is one), then a round of SORT_NT
+// slots at a time, each lane's rank among its wave's lanes of the same bucket
+// by ballots over the bucket's bits, the waves' counts added in order.
+__global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
+  __shared__ int base[MAXB], tot[MAXB];
+  __shared__ uint16_t cnt[SORT_NW][MAXB + 1];
+  __shared__ int wsum[SORT_NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = a.E + 1, b = blockIdx.x;
+  const int64_t lo = (int64_t)b * a.per, hi = min(lo + a.per, (int64_t)a.N);
+  for (int e = tid; e < B; e += SORT_NT) base[e] = tot[e] = 0;
+  __syncthreads();
+  if (a.nblk == 1) {
+    for (int s = tid; s < a.N; s += SORT_NT) atomicAdd(&tot[bucket(a, s)], 1);
+  } else {
+    // lanes along the buckets, the rest of the workgroup along the ranges (one
+    // thread for all ranges of a bucket took 40 us for 128 ranges)
+    int bp = 64;
+    while (bp < B) bp <<= 1;
+    const int parts = SORT_NT / bp ? SORT_NT / bp : 1;
+    for (int x = tid; x < bp * parts; x += SORT_NT) {
+      const int e = x & (bp - 1);
+      if (e >= B) continue;
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int q = x / bp; q < a.nblk; q += parts) {
+        const int c = a.hist[(int64_t)q * B + e];
+        all += c;
+        before += q < b ? c : 0;
+      }
+      atomicAdd(&tot[e], all);
+      atomicAdd(&base[e], before);
+    }
+  }
+  __syncthreads();
+  int first[2];
+  scan_buckets<SORT_NT>(tot, B, wsum, first);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * tid + j;
     if (e < B) {
-      const int first = excl + (j ? total[0] : 0);
-      base[e] = first + before[j];
-      if (b == 0) a.offsets[e] = first;  // offsets[E]: the first slot without an expert
+      base[e] += first[j];
+      if (b == 0) a.offsets[e] = first[j];  // offsets[E]: the first slot without an expert
     }
   }
   const int bits = 32 - __builtin_clz(B);
-  for (int s0 = lo; s0 < hi; s0 += SORT_NT) {
+  for (int64_t s0 = lo; s0 < hi; s0 += SORT_NT) {
     for (int e = lane; e < B; e += 64) cnt[wave][e] = 0;
     __syncthreads();
-    const int s = s0 + tid;
+    const int64_t s = s0 + tid;
     const bool live = s < hi;
-    const int e = live ? bucket(a, s) : 0;
+    const int e = live ? bucket(a, (int)s) : 0;
     uint64_t same = __ballot(live);
     for (int q = 0; q < bits; ++q) {
       const uint64_t m = __ballot((e >> q) & 1);
@@ -119,8 +140,8 @@ __global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
       int pos = base[e] + rank;
       for (int w = 0; w < wave; ++w) pos += cnt[w][e];
       const bool has = e < a.E;
-      a.slots[pos] = has ? s : -1;
-      a.tokens[pos] = has ? s / a.K : -1;
+      a.slots[pos] = has ? (int)s : -1;
+      a.tokens[pos] = has ? (int)s / a.K : -1;
       a.rows[s] = has ? pos : -1;
     }
     __syncthreads();
@@ -134,27 +155,108 @@ __global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
 }
 
 // ---- rows moved -------------------------------------------------------------
+constexpr int ROW_NT = 256;
+constexpr int KC = 8;  // choices that a token's workgroup ranks together
+
 struct RowArgs {
-  const void* src;
-  int64_t lds;  // in units
-  void* dst;
-  int64_t ldd;
+  const void* X;
+  int64_t ldx;
+  void* Xs;
+  int64_t lds;
   const int32_t* rows;  // [T, K]
-  int32_t T, K, n_rows;
-  int64_t units;  // per row
+  int32_t T, K, n_rows, d;
+  int32_t pieces;  // of a row, ROW_NT 16-byte units each
 };
 
-// Every choice's row a copy of its token's, in units of 16, 4, 2 or 1 bytes.
-template <typename U>
-__global__ __launch_bounds__(256) void permute_kernel(RowArgs a) {
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const U* x = (const U*)a.src + t * a.lds;
-    for (int64_t c = threadIdx.x; c < a.units; c += 256) {
-      const U v = x[c];
-      for (int k = 0; k < a.K; ++k) {
-        const int r = a.rows[t * a.K + k];
-        if ((uint32_t)r < (uint32_t)a.n_rows) ((U*)a.dst)[r * a.ldd + c] = v;
+// Piece i of the launch: token t = i / pieces, columns c0.. of this thread.
+template <int EV>
+__device__ __forceinline__ void piece_at(int64_t i, int32_t pieces, int64_t& t, int64_t& c) {
+  t = i / pieces;
+  c = ((i - t * pieces) * ROW_NT + threadIdx.x) * EV;
+}
+
+// Every choice's row a copy of its token's (E: an unsigned type of the
+// elements' size).
+template <typename E>
+__global__ __launch_bounds__(ROW_NT) void permute_kernel(RowArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E);
+  for (int64_t i = blockIdx.x; i < (int64_t)a.T * a.pieces; i += gridDim.x) {
+    int64_t t, c;
+    piece_at<EV>(i, a.pieces, t, c);
+    if (c >= a.d) continue;
+    const v4i v = sdev::load16u((const E*)a.X + t * a.ldx + c, a.d - c);
+    for (int k = 0; k < a.K; ++k) {
+      const int r = a.rows[t * a.K + k];
+      if ((uint32_t)r < (uint32_t)a.n_rows) sdev::store16u((E*)a.Xs + r * a.lds + c, v, a.d - c);
+    }
+  }
+}
+
+// The sort and the gather of few slots in one launch: every workgroup ranks
+// the slots of its token among all (a slot's row is the number of slots of
+// lower buckets and of earlier ones of its own), so none waits for another;
+// the last workgroup writes the offsets. 256 threads read at most SORT_FUSED
+// ids each from L2. (In two launches one token with 8 choices took 9.2 us.)
+template <typename E>
+__global__ __launch_bounds__(ROW_NT) void dispatch_few_kernel(SortArgs s, RowArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;
+  __shared__ int tot[MAXB], wsum[NW], pos[NW][KC];
+  __shared__ uint16_t key[SORT_FUSED];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = s.E + 1;
+  if (blockIdx.x == gridDim.x - 1) {
+    for (int e = tid; e < B; e += ROW_NT) tot[e] = 0;
+    __syncthreads();
+    for (int j = tid; j < s.N; j += ROW_NT) atomicAdd(&tot[bucket(s, j)], 1);
+    __syncthreads();
+    // 2 ROW_NT buckets at a time
+    int before = 0;
+    for (int e0 = 0; e0 < B; e0 += 2 * ROW_NT) {
+      int first[2];
+      scan_buckets<ROW_NT>(tot + e0, B - e0, wsum, first);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (e0 + 2 * tid + j < B) s.offsets[e0 + 2 * tid + j] = before + first[j];
+      for (int w = 0; w < NW; ++w) before += wsum[w];
+      __syncthreads();
+    }
+    return;
+  }
+  int64_t t, c;
+  piece_at<EV>(blockIdx.x, a.pieces, t, c);
+  const bool writes = blockIdx.x % a.pieces == 0;  // the token's first piece writes its slots
+  v4i v = {0, 0, 0, 0};
+  if (c < a.d) v = sdev::load16u((const E*)a.X + t * a.ldx + c, a.d - c);
+  for (int j = tid; j < s.N; j += ROW_NT) key[j] = (uint16_t)bucket(s, j);
+  __syncthreads();
+  for (int k0 = 0; k0 < a.K; k0 += KC) {
+    const int me = (int)t * a.K + k0;
+    int e[KC], n[KC];
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      e[k] = k0 + k < a.K ? key[me + k] : 0;
+      n[k] = 0;
+    }
+    for (int j0 = 64 * wave; j0 < s.N; j0 += ROW_NT) {
+      const int j = j0 + lane, f = j < s.N ? key[j] : MAXB;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) n[k] += __popcll(__ballot(f < e[k] || (f == e[k] && j < me + k)));
+    }
+    if (k0) __syncthreads();  // the last choices' counts are read
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < KC; ++k) pos[wave][k] = n[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      if (k0 + k >= a.K) break;
+      const int r = (pos[0][k] + pos[1][k]) + (pos[2][k] + pos[3][k]);
+      const bool has = e[k] < s.E;
+      if (writes && tid == 0) {
+        s.slots[r] = has ? me + k : -1;
+        s.tokens[r] = has ? (int)t : -1;
+        s.rows[me + k] = has ? r : -1;
       }
+      if (has && c < a.d) sdev::store16u((E*)a.Xs + r * a.lds + c, v, a.d - c);
     }
   }
 }
@@ -164,37 +266,43 @@ struct CombineArgs {
   int64_t ldo;
   const int32_t* rows;
   const float* w;  // NULL: all one
-  int32_t T, K, n_rows, d;
+  int32_t T, K, n_rows, d, pieces;
   void* Y;
   int64_t ldy;
 };
 
-template <typename E, bool VEC>
-__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  constexpr int EV = VEC ? 16 / (int)sizeof(E) : 1;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int c = threadIdx.x * EV; c < a.d; c += 256 * EV) {
-      float y[EV] = {};
-      for (int k = 0; k < a.K; ++k) {
-        const int r = a.rows[t * a.K + k];
-        if ((uint32_t)r >= (uint32_t)a.n_rows) continue;
-        const float w = a.w ? a.w[t * a.K + k] : 1.f;
-        const E* o = (const E*)a.O + r * a.ldo + c;
-        if constexpr (VEC) {
-          const v4i raw = *(const v4i*)o;
+// F rows in flight together: all eight of a few tokens, whose latency counts,
+// four of many (16384 tokens of 8 choices, 4096 bf16: 236 us, with eight 256:
+// more scattered rows are open in memory at once than it serves well).
+template <typename E, int F>
+__global__ __launch_bounds__(ROW_NT) void combine_kernel(CombineArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E);
+  for (int64_t i = blockIdx.x; i < (int64_t)a.T * a.pieces; i += gridDim.x) {
+    int64_t t, c;
+    piece_at<EV>(i, a.pieces, t, c);
+    if (c >= a.d) continue;
+    float y[EV] = {};
+    for (int k0 = 0; k0 < a.K; k0 += F) {
+      v4i raw[F];
+      float w[F];
 #pragma unroll
-          for (int e = 0; e < EV; ++e) y[e] = __builtin_fmaf(w, sdev::load_elem<E>(raw, e), y[e]);
-        } else {
-          y[0] = __builtin_fmaf(w, sdev::elem_float(o), y[0]);
+      for (int k = 0; k < F; ++k) {
+        raw[k] = v4i{0, 0, 0, 0};  // a slot without a row adds nothing, whatever its weight
+        w[k] = 0.f;
+        if (k0 + k < a.K) {  // uniform, as the next
+          const int r = a.rows[t * a.K + k0 + k];
+          if ((uint32_t)r < (uint32_t)a.n_rows) {
+            w[k] = a.w ? a.w[t * a.K + k0 + k] : 1.f;
+            raw[k] = sdev::load16u((const E*)a.O + r * a.ldo + c, a.d - c);
+          }
         }
       }
-      E* out = (E*)a.Y + t * a.ldy + c;
-      if constexpr (VEC) {
-        *(v4i*)out = sdev::pack16<E>(y);
-      } else {
-        sdev::store_elem(out, y[0]);
-      }
+#pragma unroll
+      for (int k = 0; k < F; ++k)
+#pragma unroll
+        for (int e = 0; e < EV; ++e) y[e] = __builtin_fmaf(w[k], sdev::load_elem<E>(raw[k], e), y[e]);
     }
+    sdev::store16u((E*)a.Y + t * a.ldy + c, sdev::pack16<E>(y), a.d - c);
   }
 }
 
@@ -211,44 +319,60 @@ struct CombineBwdArgs {
   float* dw;
 };
 
-template <typename E, bool VEC>
-__global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs a) {
-  constexpr int EV = VEC ? 16 / (int)sizeof(E) : 1;
-  __shared__ float red[4];
+constexpr int KG = 4;  // choices whose gradients are made together (eight: 27 us for 1500 tokens of 6 x 1111 fp32, four 23)
+
+// A workgroup per token: up to KG choices at a time, each thread's columns of
+// dY read once for them. The dot products' order is fixed: a thread's columns
+// in turn, the lanes of a wave by halves, the waves in order.
+template <typename E>
+__global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;
+  __shared__ float red[NW][KG];
+  const int tid = threadIdx.x;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const E* dy = (const E*)a.dY + t * a.lddy;
-    for (int k = 0; k < a.K; ++k) {
-      const int r = a.rows[t * a.K + k];
-      const bool has = (uint32_t)r < (uint32_t)a.n_rows;
-      const float w = a.w[t * a.K + k];
-      float dot = 0.f;
-      if (has) {
-        const E* o = (const E*)a.O + r * a.ldo;
-        E* g = (E*)a.dO + r * a.lddo;
-        for (int c = threadIdx.x * EV; c < a.d; c += 256 * EV) {
-          if constexpr (VEC) {
-            const v4i ry = *(const v4i*)(dy + c), ro = *(const v4i*)(o + c);
-            float v[EV];
+    for (int k0 = 0; k0 < a.K; k0 += KG) {
+      int r[KG];
+      float w[KG], dot[KG];
 #pragma unroll
-            for (int e = 0; e < EV; ++e) {
-              const float y = sdev::load_elem<E>(ry, e);
-              dot = __builtin_fmaf(y, sdev::load_elem<E>(ro, e), dot);
-              v[e] = w * y;
-            }
-            *(v4i*)(g + c) = sdev::pack16<E>(v);
-          } else {
-            const float y = sdev::elem_float(dy + c);
-            dot = __builtin_fmaf(y, sdev::elem_float(o + c), dot);
-            sdev::store_elem(g + c, w * y);
+      for (int k = 0; k < KG; ++k) {
+        r[k] = k0 + k < a.K ? a.rows[t * a.K + k0 + k] : -1;
+        w[k] = k0 + k < a.K ? a.w[t * a.K + k0 + k] : 0.f;
+        dot[k] = 0.f;
+      }
+      for (int64_t c = tid * EV; c < a.d; c += ROW_NT * EV) {
+        const v4i ry = sdev::load16u(dy + c, a.d - c);
+        v4i ro[KG];
+#pragma unroll
+        for (int k = 0; k < KG; ++k)
+          if ((uint32_t)r[k] < (uint32_t)a.n_rows) ro[k] = sdev::load16u((const E*)a.O + r[k] * a.ldo + c, a.d - c);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          if ((uint32_t)r[k] >= (uint32_t)a.n_rows) continue;  // uniform
+          float v[EV];
+#pragma unroll
+          for (int e = 0; e < EV; ++e) {
+            const float y = sdev::load_elem<E>(ry, e);
+            dot[k] = __builtin_fmaf(y, sdev::load_elem<E>(ro[k], e), dot[k]);
+            v[e] = w[k] * y;
           }
+          sdev::store16u((E*)a.dO + r[k] * a.lddo + c, sdev::pack16<E>(v), a.d - c);
         }
       }
 #pragma unroll
-      for (int m = 32; m; m >>= 1) dot += __shfl_xor(dot, m, 64);
+      for (int k = 0; k < KG; ++k)
+#pragma unroll
+        for (int m = 32; m; m >>= 1) dot[k] += __shfl_xor(dot[k], m, 64);
+      __syncthreads();  // the last sums are read
+      if ((tid & 63) == 0)
+#pragma unroll
+        for (int k = 0; k < KG; ++k) red[tid >> 6][k] = dot[k];
       __syncthreads();
-      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) a.dw[t * a.K + k] = has ? (red[0] + red[1]) + (red[2] + red[3]) : 0.f;
+      if (tid < KG && k0 + tid < a.K) {
+        float s = 0.f;
+        for (int q = 0; q < NW; ++q) s += red[q][tid];
+        a.dw[t * a.K + k0 + tid] = s;
+      }
     }
   }
 }
@@ -274,26 +398,37 @@ void sort_plan(int64_t N, int32_t* nblk, int32_t* per) {
   *nblk = (int32_t)((N + *per - 1) / *per);
 }
 
-template <typename U>
-int launch_permute_t(const RowArgs& a, hipStream_t st) {
-  permute_kernel<U><<<dim3(row_grid(a.T)), dim3(256), 0, st>>>(a);
+// Pieces of a row of d elements of eb bytes, and workgroups for T tokens.
+int32_t row_pieces(int32_t d, int eb) {
+  const int64_t per = (int64_t)ROW_NT * 16 / eb;
+  return (int32_t)((d + per - 1) / per);
+}
+unsigned piece_grid(int32_t T, int32_t pieces) {
+  const int64_t n = (int64_t)T * pieces;
+  return (unsigned)(n < (1 << 22) ? n : 1 << 22);
+}
+
+RowArgs row_args(int32_t eb, const void* X, int64_t ldx, int32_t T, int32_t K, int32_t d, const int32_t* rows, void* Xs,
+                 int64_t lds) {
+  return RowArgs{X, ldx, Xs, lds, rows, T, K, T * K, d, row_pieces(d, eb)};
+}
+
+int launch_permute(int32_t eb, const RowArgs& a, hipStream_t st) {
+  const dim3 grid(piece_grid(a.T, a.pieces)), block(ROW_NT);
+  if (eb == 4) permute_kernel<uint32_t><<<grid, block, 0, st>>>(a);
+  else if (eb == 2) permute_kernel<uint16_t><<<grid, block, 0, st>>>(a);
+  else permute_kernel<uint8_t><<<grid, block, 0, st>>>(a);
   const int rc = fpi::check_launch("permute_kernel");
   return rc ? rc : fpi::ok();
 }
 
-// The widest unit that the rows' sizes, strides and addresses are whole in.
-int launch_permute(int32_t eb, const void* X, int64_t ldx, int32_t T, int32_t K, int32_t d, const int32_t* rows, void* Xs,
-                   int64_t lds, hipStream_t st) {
-  RowArgs a{X, 0, Xs, 0, rows, T, K, T * K, 0};
-  const uintptr_t all = (uintptr_t)X | (uintptr_t)Xs | (uintptr_t)((int64_t)d * eb) | (uintptr_t)(ldx * eb) | (uintptr_t)(lds * eb);
-  const int u = all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : (all % 2 == 0 ? 2 : 1));
-  a.lds = ldx * eb / u;
-  a.ldd = lds * eb / u;
-  a.units = (int64_t)d * eb / u;
-  if (u == 16) return launch_permute_t<v4i>(a, st);
-  if (u == 4) return launch_permute_t<uint32_t>(a, st);
-  if (u == 2) return launch_permute_t<uint16_t>(a, st);
-  return launch_permute_t<uint8_t>(a, st);
+int launch_dispatch_few(int32_t eb, const SortArgs& s, const RowArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.T * a.pieces + 1)), block(ROW_NT);
+  if (eb == 4) dispatch_few_kernel<uint32_t><<<grid, block, 0, st>>>(s, a);
+  else if (eb == 2) dispatch_few_kernel<uint16_t><<<grid, block, 0, st>>>(s, a);
+  else dispatch_few_kernel<uint8_t><<<grid, block, 0, st>>>(s, a);
+  const int rc = fpi::check_launch("dispatch_few_kernel");
+  return rc ? rc : fpi::ok();
 }
 
 int launch_sort(SortArgs a, hipStream_t st) {
@@ -363,7 +498,7 @@ extern "C" int fp_moe_permute(int32_t elem_bytes, const void* X, int64_t ldx, in
   const int rc = check_permute("fp_moe_permute", elem_bytes, X, ldx, T, K, d, rows, Xs, lds);
   if (rc) return rc;
   if (T == 0 || d == 0) return fpi::ok();
-  return launch_permute(elem_bytes, X, ldx, T, K, d, rows, Xs, lds, stream);
+  return launch_permute(elem_bytes, row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds), stream);
 }
 
 extern "C" int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, int32_t d, const void* ids,
@@ -373,9 +508,13 @@ extern "C" int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, i
   const char* fn = "fp_moe_dispatch";
   int rc = check_sort(fn, ids, id_bytes, T, K, E, offsets, slots, tokens, rows, ws, ws_bytes);
   if (rc || (rc = check_permute(fn, elem_bytes, X, ldx, T, K, d, rows, Xs, lds))) return rc;
-  rc = launch_sort(SortArgs{ids, id_bytes == 8, T * K, K, E, 0, 0, offsets, slots, tokens, rows, (int32_t*)ws}, stream);
+  const SortArgs sa{ids, id_bytes == 8, T * K, K, E, 0, 0, offsets, slots, tokens, rows, (int32_t*)ws};
+  const RowArgs ra = row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds);
+  // few slots in one launch: every workgroup reads all ids for each of its token's choices
+  if (T > 0 && d > 0 && T * K <= SORT_FUSED && K <= 16) return launch_dispatch_few(elem_bytes, sa, ra, stream);
+  rc = launch_sort(sa, stream);
   if (rc || T == 0 || d == 0) return rc;
-  return launch_permute(elem_bytes, X, ldx, T, K, d, rows, Xs, lds, stream);
+  return launch_permute(elem_bytes, ra, stream);
 }
 
 extern "C" int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n_rows, const int32_t* rows,
@@ -390,12 +529,12 @@ extern "C" int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n
   if ((rc = check_rows(fn, O, ldo, d, eb)) || (rc = check_rows(fn, Y, ldy, d, eb))) return rc;
   if (T == 0 || d == 0) return fpi::ok();
   if ((n_rows > 0 && !O) || !rows || !Y) return fpi::fail(FP_EARG, "%s: null pointer", fn);
-  const CombineArgs a{O, ldo, rows, w, T, K, n_rows, d, Y, ldy};
-  const bool vec = (((uintptr_t)O | (uintptr_t)Y | (uintptr_t)(ldo * eb) | (uintptr_t)(ldy * eb) | (uintptr_t)((int64_t)d * eb)) & 15) == 0;
-  const dim3 grid(row_grid(T)), block(256);
-  if (dt == FP_F32) vec ? combine_kernel<float, true><<<grid, block, 0, stream>>>(a) : combine_kernel<float, false><<<grid, block, 0, stream>>>(a);
-  else if (dt == FP_F16) vec ? combine_kernel<__half, true><<<grid, block, 0, stream>>>(a) : combine_kernel<__half, false><<<grid, block, 0, stream>>>(a);
-  else vec ? combine_kernel<__hip_bfloat16, true><<<grid, block, 0, stream>>>(a) : combine_kernel<__hip_bfloat16, false><<<grid, block, 0, stream>>>(a);
+  const CombineArgs a{O, ldo, rows, w, T, K, n_rows, d, row_pieces(d, eb), Y, ldy};
+  const dim3 grid(piece_grid(T, a.pieces)), block(ROW_NT);
+  const bool few = grid.x <= 1024;
+  if (dt == FP_F32) few ? combine_kernel<float, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<float, 4><<<grid, block, 0, stream>>>(a);
+  else if (dt == FP_F16) few ? combine_kernel<__half, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<__half, 4><<<grid, block, 0, stream>>>(a);
+  else few ? combine_kernel<__hip_bfloat16, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<__hip_bfloat16, 4><<<grid, block, 0, stream>>>(a);
   rc = fpi::check_launch("combine_kernel");
   return rc ? rc : fpi::ok();
 }
@@ -413,12 +552,10 @@ extern "C" int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy
   if (T == 0) return fpi::ok();
   if (!rows || !w || !dw || (d > 0 && (!dY || (n_rows > 0 && (!O || !dO))))) return fpi::fail(FP_EARG, "%s: null pointer", fn);
   const CombineBwdArgs a{dY, lddy, O, ldo, rows, w, T, K, n_rows, d, dO, lddo, dw};
-  const bool vec = (((uintptr_t)dY | (uintptr_t)O | (uintptr_t)dO | (uintptr_t)(lddy * eb) | (uintptr_t)(ldo * eb) | (uintptr_t)(lddo * eb) |
-                     (uintptr_t)((int64_t)d * eb)) & 15) == 0;
-  const dim3 grid(row_grid(T)), block(256);
-  if (dt == FP_F32) vec ? combine_backward_kernel<float, true><<<grid, block, 0, stream>>>(a) : combine_backward_kernel<float, false><<<grid, block, 0, stream>>>(a);
-  else if (dt == FP_F16) vec ? combine_backward_kernel<__half, true><<<grid, block, 0, stream>>>(a) : combine_backward_kernel<__half, false><<<grid, block, 0, stream>>>(a);
-  else vec ? combine_backward_kernel<__hip_bfloat16, true><<<grid, block, 0, stream>>>(a) : combine_backward_kernel<__hip_bfloat16, false><<<grid, block, 0, stream>>>(a);
+  const dim3 grid(row_grid(T)), block(ROW_NT);
+  if (dt == FP_F32) combine_backward_kernel<float><<<grid, block, 0, stream>>>(a);
+  else if (dt == FP_F16) combine_backward_kernel<__half><<<grid, block, 0, stream>>>(a);
+  else combine_backward_kernel<__hip_bfloat16><<<grid, block, 0, stream>>>(a);
   rc = fpi::check_launch("combine_backward_kernel");
   return rc ? rc : fpi::ok();
 }

@@ -67,6 +67,57 @@ __device__ __forceinline__ void store_elem(E* p, float f) {
   else *(unsigned short*)p = (unsigned short)Out<E>::bits(f);
 }
 
+// 16 bytes at any element's address.
+template <int EB>
+struct AnyVec;
+template <>
+struct AnyVec<4> {
+  typedef int type __attribute__((ext_vector_type(4), aligned(4), may_alias));
+};
+template <>
+struct AnyVec<2> {
+  typedef int type __attribute__((ext_vector_type(4), aligned(2), may_alias));
+};
+template <>
+struct AnyVec<1> {
+  typedef int type __attribute__((ext_vector_type(4), aligned(1), may_alias));
+};
+
+// Elements at p, n of them if fewer than 16 bytes hold (the rest zero). The
+// address needs the alignment of an element only: one 16-byte load, which the
+// hardware takes at any address.
+template <typename E>
+__device__ __forceinline__ v4i load16u(const E* p, int64_t n) {
+  constexpr int EV = 16 / (int)sizeof(E);
+  typedef typename AnyVec<sizeof(E)>::type vec;
+  if (n >= EV) return *(const vec*)p;
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < EV; ++e)
+    if (e < n) {
+      if constexpr (sizeof(E) == 4) w[e] = *(const uint32_t*)(p + e);
+      else if constexpr (sizeof(E) == 2) w[e / 2] |= (uint32_t)*(const uint16_t*)(p + e) << (16 * (e % 2));
+      else w[e / 4] |= (uint32_t)*(const uint8_t*)(p + e) << (8 * (e % 4));
+    }
+  return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+}
+template <typename E>
+__device__ __forceinline__ void store16u(E* p, const v4i& v, int64_t n) {
+  constexpr int EV = 16 / (int)sizeof(E);
+  typedef typename AnyVec<sizeof(E)>::type vec;
+  if (n >= EV) {
+    *(vec*)p = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < EV; ++e)
+    if (e < n) {
+      if constexpr (sizeof(E) == 4) *(uint32_t*)(p + e) = (uint32_t)v[e];
+      else if constexpr (sizeof(E) == 2) *(uint16_t*)(p + e) = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e % 2)));
+      else *(uint8_t*)(p + e) = (uint8_t)((uint32_t)v[e / 4] >> (8 * (e % 4)));
+    }
+}
+
 // 16 bytes of rounded elements.
 template <typename E>
 __device__ __forceinline__ v4i pack16(const float* v) {
