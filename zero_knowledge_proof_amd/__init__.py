@@ -237,6 +237,11 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# the same without a Stream object (4 us a call), where torch offers it
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _dev():
     return torch.device("cuda", torch.cuda.current_device())
 
@@ -618,38 +623,48 @@ def _float_dt(dtype, name: str) -> int:
     return dt
 
 
-def _matrix(t, dtype, rows, cols: int, name: str):
+def _matrix(t, dtype, rows, cols: int, name: str) -> int:
     """Check a row-major device matrix: dtype (None: any), shape (rows None: any) and unit column stride; a matrix that
-    is written (or read) row by row has rows that do not overlap."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != cols:
-        raise ValueError("%s: shape %s, expected (%s, %d)" % (name, tuple(t.shape), "*" if rows is None else rows, cols))
-    if dtype is not None and t.dtype != dtype:
+    is written (or read) row by row has rows that do not overlap. Returns its leading dimension."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError("%s: shape %s, expected (%s, %d)" % (name, tuple(shape), "*" if rows is None else rows, cols))
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.numel() and ((cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols)):
+    ld = stride[0]
+    if shape[0] > 1:
+        if cols and ((cols > 1 and stride[1] != 1) or ld < cols):
+            raise ValueError("%s: rows must be contiguous and must not overlap" % name)
+        return ld
+    if cols > 1 and stride[1] != 1 and shape[0]:
         raise ValueError("%s: rows must be contiguous and must not overlap" % name)
+    return max(ld, cols)
 
 
 def _vector(t, dtype, shape, name: str):
     """Check a dense device array of this dtype and shape."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError("%s: %s %s, expected %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s: must be contiguous" % name)
 
 
-def _here(*named):
-    """Every given tensor is on the current device, where the call's stream and its scratch are."""
-    dev = torch.cuda.current_device()
-    for t in named:
-        if t is not None and not (t.is_cuda and t.get_device() == dev):
+def _here(*tensors) -> int:
+    """The current device's current stream; every given tensor is on that device, where the call runs."""
+    dev = _device_index()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, dev))
+    return _raw_stream(dev)
 
 
 def _whole_rows(X):
     """X's rows, when they start on 16 bytes, are read in whole 16-byte chunks: the last row's must be in its storage."""
     T, d = X.shape
+    if d % 16 == 0:
+        return
     ld, up = _ld(X), (d + 15) // 16 * 16
-    if up != d and ld % 16 == 0 and X.data_ptr() % 16 == 0 and ld >= up:
+    if ld % 16 == 0 and X.data_ptr() % 16 == 0 and ld >= up:
         end = X.storage_offset() + (T - 1) * ld + up
         if T and end > X.untyped_storage().nbytes():
             raise ValueError("X: the last row is read up to column %d, past its storage (copy X, or pad its rows)" % up)
@@ -663,69 +678,71 @@ def quantize_rows(X, out=None, scale=None):
         raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
     T, d = X.shape
     dt = _float_dt(X.dtype, "X")
-    _matrix(X, None, T, d, "X")
+    ldx = _matrix(X, None, T, d, "X")
     if out is None:
-        out = torch.empty((T, (d + 15) // 16 * 16), dtype=torch.int8, device=X.device)[:, :d]
-    else:
-        _matrix(out, torch.int8, T, d, "out")
+        out = torch.empty((T, (d + 15) // 16 * 16), dtype=torch.int8, device=X.device)
+        if d % 16:
+            out = out[:, :d]
+    ldq = _matrix(out, torch.int8, T, d, "out")
     if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=X.device)
     else:
         _vector(scale, torch.float32, (T,), "scale")
-    _here(X, out, scale)
-    _check(lib().fp_quantize_rows(dt, X.data_ptr(), _ld(X), T, d, out.data_ptr(), _ld(out), scale.data_ptr(),
-                                  _stream()), "fp_quantize_rows")
+    st = _here(X, out, scale)
+    _check(lib().fp_quantize_rows(dt, X.data_ptr(), ldx, T, d, out.data_ptr(), ldq, scale.data_ptr(), st),
+           "fp_quantize_rows")
     return out, scale
 
 
 def _product_out(T, d_out, out, dtype, Z, device):
+    """out (made if None), its type, its leading dimension, Z's address and leading dimension."""
     if out is None:
+        _float_dt(dtype, "out")
         out = torch.empty((T, d_out), dtype=dtype, device=device)
-    else:
-        _matrix(out, None, T, d_out, "out")
+    ldy = _matrix(out, None, T, d_out, "out")
     dt = _float_dt(out.dtype, "out")
-    if Z is not None:
-        _matrix(Z, torch.int32, T, d_out, "Z")
-    return out, dt, (0 if Z is None else Z.data_ptr()), (d_out if Z is None else _ld(Z))
+    if Z is None:
+        return out, dt, ldy, 0, d_out
+    return out, dt, ldy, Z.data_ptr(), _matrix(Z, torch.int32, T, d_out, "Z")
 
 
 def scaled_matmul(X, x_scale, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=torch.bfloat16, Z=None):
     """Y[t, o] = x_scale[t] w_scale[o] sum_k X[t, k] W[o, k] + bias[o] for int8 X [T, d_in] and packed weights, in
     ``out``'s type or ``dtype``; Z (int32 [T, d_out] or None) also receives the integer product, the layer's witness."""
-    _matrix(X, torch.int8, None, Wp.d_in, "X")
-    T, d_out = X.shape[0], Wp.d_out
+    d_in, d_out = Wp.d_in, Wp.d_out
+    ldx = _matrix(X, torch.int8, None, d_in, "X")
+    T = X.shape[0]
     _vector(x_scale, torch.float32, (T,), "x_scale")
     _vector(w_scale, torch.float32, (d_out,), "w_scale")
     if bias is not None:
         _vector(bias, torch.float32, (d_out,), "bias")
-    out, dt, z, ldz = _product_out(T, d_out, out, dtype, Z, X.device)
-    _here(X, x_scale, Wp.data, w_scale, bias, out, Z)
+    out, dt, ldy, z, ldz = _product_out(T, d_out, out, dtype, Z, X.device)
     _whole_rows(X)
-    _check(lib().fp_scaled_matmul(X.data_ptr(), _ld(X), x_scale.data_ptr(), Wp.data.data_ptr(), w_scale.data_ptr(),
-                                  0 if bias is None else bias.data_ptr(), T, Wp.d_in, d_out, dt, out.data_ptr(),
-                                  _ld(out), z, ldz, _stream()), "fp_scaled_matmul")
+    st = _here(X, x_scale, Wp.data, w_scale, bias, out, Z)
+    _check(lib().fp_scaled_matmul(X.data_ptr(), ldx, x_scale.data_ptr(), Wp.data.data_ptr(), w_scale.data_ptr(),
+                                  0 if bias is None else bias.data_ptr(), T, d_in, d_out, dt, out.data_ptr(), ldy, z,
+                                  ldz, st), "fp_scaled_matmul")
     return out
 
 
 def scaled_linear(X, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=None, Z=None):
     """scaled_matmul of quantize_rows(X) for X [T, d_in] in float32, float16 or bfloat16; the answer is in ``out``'s
     type, ``dtype`` or X's."""
-    if X.dim() != 2 or X.shape[1] != Wp.d_in:
-        raise ValueError("X: shape %s, expected (*, %d)" % (tuple(X.shape), Wp.d_in))
+    d_in, d_out = Wp.d_in, Wp.d_out
+    ldx = _matrix(X, None, None, d_in, "X")
     x_dt = _float_dt(X.dtype, "X")
-    _matrix(X, None, None, Wp.d_in, "X")
-    T, d_out = X.shape[0], Wp.d_out
+    T = X.shape[0]
     _vector(w_scale, torch.float32, (d_out,), "w_scale")
     if bias is not None:
         _vector(bias, torch.float32, (d_out,), "bias")
-    out, dt, z, ldz = _product_out(T, d_out, out, dtype or X.dtype, Z, X.device)
-    _here(X, Wp.data, w_scale, bias, out, Z)
-    nbytes = lib().fp_scaled_linear_workspace(T, Wp.d_in)
+    out, dt, ldy, z, ldz = _product_out(T, d_out, out, dtype or X.dtype, Z, X.device)
+    st = _here(X, Wp.data, w_scale, bias, out, Z)
+    nbytes = lib().fp_scaled_linear_workspace(T, d_in)
     # from the allocator each time, which keeps scratch of different streams and captured graphs apart
     ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
-    _check(lib().fp_scaled_linear(x_dt, X.data_ptr(), _ld(X), Wp.data.data_ptr(), w_scale.data_ptr(),
-                                  0 if bias is None else bias.data_ptr(), T, Wp.d_in, d_out, dt, out.data_ptr(),
-                                  _ld(out), z, ldz, ws.data_ptr(), nbytes, _stream()), "fp_scaled_linear")
+    _check(lib().fp_scaled_linear(x_dt, X.data_ptr(), ldx, Wp.data.data_ptr(), w_scale.data_ptr(),
+                                  0 if bias is None else bias.data_ptr(), T, d_in, d_out, dt, out.data_ptr(), ldy, z,
+                                  ldz, ws.data_ptr(), nbytes, st), "fp_scaled_linear")
     return out
 
 
@@ -759,28 +776,24 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
     device, as moe_sort writes them) by expert g with w_scale[g] (float32 [G, d_out]; bias likewise). Output row i is
     made from X's row rows[i] (int32 on the device, e.g. moe_sort's tokens; None: row i). Rows of no expert are left as
     they were in ``out`` and Z (a new ``out`` holds whatever its memory held there)."""
-    G, d_out = len(We), We.d_out
-    _matrix(X, torch.int8, None, We.d_in, "X")
-    x_rows = X.shape[0]
+    G, d_in, d_out = len(We.weights), We.d_in, We.d_out
+    ldx = _matrix(X, torch.int8, None, d_in, "X")
+    n = x_rows = X.shape[0]
     _vector(x_scale, torch.float32, (x_rows,), "x_scale")
-    _matrix(w_scale, torch.float32, G, d_out, "w_scale")
-    if bias is not None:
-        _matrix(bias, torch.float32, G, d_out, "bias")
-        if _ld(bias) != _ld(w_scale):
-            raise ValueError("bias: row stride %d, w_scale has %d" % (_ld(bias), _ld(w_scale)))
+    ldw = _matrix(w_scale, torch.float32, G, d_out, "w_scale")
+    if bias is not None and _matrix(bias, torch.float32, G, d_out, "bias") != ldw:
+        raise ValueError("bias: its rows are not as far apart as w_scale's")
     _vector(offsets, torch.int32, (G + 1,), "offsets")
-    n = x_rows
     if rows is not None:
         n = rows.numel()
         _vector(rows, torch.int32, (n,), "rows")
-    out, dt, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
-    _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
+    out, dt, ldy, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
     _whole_rows(X)
-    _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), _ld(X), x_scale.data_ptr(), x_rows,
+    st = _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
+    _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), ldx, x_scale.data_ptr(), x_rows,
                                           0 if rows is None else rows.data_ptr(), n, We.ptrs, w_scale.data_ptr(),
-                                          0 if bias is None else bias.data_ptr(), _ld(w_scale), offsets.data_ptr(), G,
-                                          We.d_in, d_out, dt, out.data_ptr(), _ld(out), z, ldz, _stream()),
-           "fp_scaled_matmul_grouped")
+                                          0 if bias is None else bias.data_ptr(), ldw, offsets.data_ptr(), G, d_in,
+                                          d_out, dt, out.data_ptr(), ldy, z, ldz, st), "fp_scaled_matmul_grouped")
     return out
 
 
@@ -803,6 +816,8 @@ class MoePlan:
         self.rows = buf[E + 1 + 2 * n:E + 1 + 3 * n].view(T, K)
         self.ws = buf[E + 1 + 3 * n:]
         self.buf = buf
+        # offsets, slots, tokens, rows: where the calls write them
+        self.ptrs = tuple(t.data_ptr() for t in (self.offsets, self.slots, self.tokens, self.rows))
 
 
 def _sort_args(ids, n_experts: int, plan):
@@ -822,45 +837,44 @@ def moe_sort(ids, n_experts: int, plan: MoePlan | None = None) -> MoePlan:
     """The slots of ids [T, K] (each token's experts, int32 or int64 on the device) sorted by expert, stably; an id
     outside [0, n_experts) is a slot without an expert. Nothing is read back by the host (compare moe_plan)."""
     plan = _sort_args(ids, n_experts, plan)
-    _here(ids, plan.buf)
-    _check(lib().fp_moe_sort(ids.data_ptr(), ids.element_size(), plan.T, plan.K, plan.E, plan.offsets.data_ptr(),
-                             plan.slots.data_ptr(), plan.tokens.data_ptr(), plan.rows.data_ptr(), plan.ws.data_ptr(),
-                             plan.nbytes, _stream()), "fp_moe_sort")
+    st = _here(ids, plan.buf)
+    _check(lib().fp_moe_sort(ids.data_ptr(), ids.element_size(), plan.T, plan.K, plan.E, *plan.ptrs,
+                             plan.ws.data_ptr(), plan.nbytes, st), "fp_moe_sort")
     return plan
 
 
 def _permute_out(X, plan, out):
-    if X.element_size() not in (1, 2, 4):
-        raise ValueError("X: elements of %d bytes, expected 1, 2 or 4" % X.element_size())
+    """X's element size and leading dimension, out (made if None) and its leading dimension."""
+    eb = X.element_size()
+    if eb not in (1, 2, 4):
+        raise ValueError("X: elements of %d bytes, expected 1, 2 or 4" % eb)
     if X.dim() != 2:
         raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
-    d = X.shape[1]
-    _matrix(X, None, plan.T, d, "X")
+    d, n = X.shape[1], plan.T * plan.K
+    ldx = _matrix(X, None, plan.T, d, "X")
     if out is None:
-        return torch.empty((plan.T * plan.K, d), dtype=X.dtype, device=X.device)
-    _matrix(out, X.dtype, plan.T * plan.K, d, "out")
-    return out
+        out = torch.empty((n, d), dtype=X.dtype, device=X.device)
+    return eb, ldx, out, _matrix(out, X.dtype, n, d, "out")
 
 
 def moe_permute(X, plan: MoePlan, out=None):
     """Xs [T K, d]: the tokens' rows X [T, d] in the plan's order. Rows past the last one with an expert are left as
     they were in ``out`` (a new one holds whatever its memory held there)."""
-    out = _permute_out(X, plan, out)
-    _here(X, plan.buf, out)
-    _check(lib().fp_moe_permute(X.element_size(), X.data_ptr(), _ld(X), plan.T, plan.K, X.shape[1],
-                                plan.rows.data_ptr(), out.data_ptr(), _ld(out), _stream()), "fp_moe_permute")
+    eb, ldx, out, ldo = _permute_out(X, plan, out)
+    st = _here(X, plan.buf, out)
+    _check(lib().fp_moe_permute(eb, X.data_ptr(), ldx, plan.T, plan.K, X.shape[1], plan.ptrs[3], out.data_ptr(), ldo,
+                                st), "fp_moe_permute")
     return out
 
 
 def moe_dispatch(X, ids, n_experts: int, plan: MoePlan | None = None, out=None):
     """(Xs, plan): moe_sort of ids and moe_permute of X in one call."""
     plan = _sort_args(ids, n_experts, plan)
-    out = _permute_out(X, plan, out)
-    _here(X, ids, plan.buf, out)
-    _check(lib().fp_moe_dispatch(X.element_size(), X.data_ptr(), _ld(X), X.shape[1], ids.data_ptr(),
-                                 ids.element_size(), plan.T, plan.K, plan.E, plan.offsets.data_ptr(),
-                                 plan.slots.data_ptr(), plan.tokens.data_ptr(), plan.rows.data_ptr(), out.data_ptr(),
-                                 _ld(out), plan.ws.data_ptr(), plan.nbytes, _stream()), "fp_moe_dispatch")
+    eb, ldx, out, ldo = _permute_out(X, plan, out)
+    st = _here(X, ids, plan.buf, out)
+    _check(lib().fp_moe_dispatch(eb, X.data_ptr(), ldx, X.shape[1], ids.data_ptr(), ids.element_size(), plan.T, plan.K,
+                                 plan.E, *plan.ptrs, out.data_ptr(), ldo, plan.ws.data_ptr(), plan.nbytes, st),
+           "fp_moe_dispatch")
     return out, plan
 
 
@@ -869,17 +883,16 @@ def _combine(O, plan, weights, out, name):
         raise ValueError("%s: shape %s, expected two dimensions" % (name, tuple(O.shape)))
     T, K, d = plan.T, plan.K, O.shape[1]
     dt = _float_dt(O.dtype, name)
-    _matrix(O, None, T * K, d, name)
+    ldi = _matrix(O, None, T * K, d, name)
     if weights is not None:
         _vector(weights, torch.float32, (T, K), "weights")
     if out is None:
         out = torch.empty((T, d), dtype=O.dtype, device=O.device)
-    else:
-        _matrix(out, O.dtype, T, d, "out")
-    _here(O, plan.buf, weights, out)
-    _check(lib().fp_moe_combine(dt, O.data_ptr(), _ld(O), T * K, plan.rows.data_ptr(),
-                                0 if weights is None else weights.data_ptr(), T, K, d, out.data_ptr(), _ld(out),
-                                _stream()), "fp_moe_combine")
+    ldo = _matrix(out, O.dtype, T, d, "out")
+    st = _here(O, plan.buf, weights, out)
+    _check(lib().fp_moe_combine(dt, O.data_ptr(), ldi, T * K, plan.ptrs[3],
+                                0 if weights is None else weights.data_ptr(), T, K, d, out.data_ptr(), ldo, st),
+           "fp_moe_combine")
     return out
 
 
@@ -901,20 +914,18 @@ def moe_combine_backward(dY, O, plan: MoePlan, weights, dO=None, dw=None):
         raise ValueError("O: shape %s, expected two dimensions" % (tuple(O.shape),))
     T, K, d = plan.T, plan.K, O.shape[1]
     dt = _float_dt(O.dtype, "O")
-    _matrix(O, None, T * K, d, "O")
-    _matrix(dY, O.dtype, T, d, "dY")
+    ldi, ldy = _matrix(O, None, T * K, d, "O"), _matrix(dY, O.dtype, T, d, "dY")
     _vector(weights, torch.float32, (T, K), "weights")
     if dO is None:
         dO = torch.empty((T * K, d), dtype=O.dtype, device=O.device)
-    else:
-        _matrix(dO, O.dtype, T * K, d, "dO")
+    ldo = _matrix(dO, O.dtype, T * K, d, "dO")
     if dw is None:
         dw = torch.empty((T, K), dtype=torch.float32, device=O.device)
     else:
         _vector(dw, torch.float32, (T, K), "dw")
-    _here(dY, O, plan.buf, weights, dO, dw)
-    _check(lib().fp_moe_combine_backward(dt, dY.data_ptr(), _ld(dY), O.data_ptr(), _ld(O), T * K, plan.rows.data_ptr(),
-                                         weights.data_ptr(), T, K, d, dO.data_ptr(), _ld(dO), dw.data_ptr(), _stream()),
+    st = _here(dY, O, plan.buf, weights, dO, dw)
+    _check(lib().fp_moe_combine_backward(dt, dY.data_ptr(), ldy, O.data_ptr(), ldi, T * K, plan.ptrs[3],
+                                         weights.data_ptr(), T, K, d, dO.data_ptr(), ldo, dw.data_ptr(), st),
            "fp_moe_combine_backward")
     return dO, dw
 

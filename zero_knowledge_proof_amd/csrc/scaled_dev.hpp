@@ -83,6 +83,9 @@ struct AnyVec<1> {
   typedef int type __attribute__((ext_vector_type(4), aligned(1), may_alias));
 };
 
+typedef int AnyWord __attribute__((aligned(1), may_alias));
+typedef int AnyPair __attribute__((ext_vector_type(2), aligned(1), may_alias));
+
 // Elements at p, n of them if fewer than 16 bytes hold (the rest zero). The
 // address needs the alignment of an element only: one 16-byte load, which the
 // hardware takes at any address.
