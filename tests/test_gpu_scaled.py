@@ -79,6 +79,17 @@ def test_scaled_matmul_any_rows(fp, T, d_in, d_out, pad, offset):
     close(y, Y, mag, torch.float32)
 
 
+def test_one_row_at_the_end_of_its_storage(fp):
+    """A single row whose last 16-byte chunk would leave its storage is read byte by byte."""
+    rng = np.random.default_rng(8)
+    _, W, _, ws, _ = inputs(rng, 1, 100, 70)
+    buf = torch.from_numpy(rng.integers(-128, 128, size=3 * 128 + 100, dtype=np.int8)).cuda()
+    X = torch.as_strided(buf, (1, 100), (128, 1), 3 * 128)
+    xs = torch.ones(1, device="cuda")
+    Z, Y, mag = reference(X, W, xs, ws)
+    close(fp.scaled_matmul(X, xs, fp.pack_weights(W), ws, dtype=torch.float32), Y, mag, torch.float32)
+
+
 @pytest.mark.parametrize("T,d_out", [(1, 96), (9, 100), (40, 31), (150, 260)])
 @pytest.mark.parametrize("dt", TYPES)
 def test_scaled_matmul_strided_out(fp, T, d_out, dt):

@@ -658,16 +658,17 @@ def _here(*tensors) -> int:
     return _raw_stream(dev)
 
 
-def _whole_rows(X):
-    """X's rows, when they start on 16 bytes, are read in whole 16-byte chunks: the last row's must be in its storage."""
+def _whole_rows(X, ld: int) -> int:
+    """X's rows, when they start on 16 bytes, are read in whole 16-byte chunks: the last row's must be in its storage.
+    Returns the leading dimension to pass: a single row without the bytes for its last chunk is read byte by byte."""
     T, d = X.shape
-    if d % 16 == 0:
-        return
-    ld, up = _ld(X), (d + 15) // 16 * 16
-    if ld % 16 == 0 and X.data_ptr() % 16 == 0 and ld >= up:
-        end = X.storage_offset() + (T - 1) * ld + up
-        if T and end > X.untyped_storage().nbytes():
+    up = (d + 15) // 16 * 16
+    if up != d and T and ld >= up and ld % 16 == 0 and X.data_ptr() % 16 == 0:
+        if X.storage_offset() + (T - 1) * ld + up > X.untyped_storage().nbytes():
+            if T == 1:
+                return d
             raise ValueError("X: the last row is read up to column %d, past its storage (copy X, or pad its rows)" % up)
+    return ld
 
 
 def quantize_rows(X, out=None, scale=None):
@@ -717,7 +718,7 @@ def scaled_matmul(X, x_scale, Wp: PackedWeights, w_scale, bias=None, out=None, d
     if bias is not None:
         _vector(bias, torch.float32, (d_out,), "bias")
     out, dt, ldy, z, ldz = _product_out(T, d_out, out, dtype, Z, X.device)
-    _whole_rows(X)
+    ldx = _whole_rows(X, ldx)
     st = _here(X, x_scale, Wp.data, w_scale, bias, out, Z)
     _check(lib().fp_scaled_matmul(X.data_ptr(), ldx, x_scale.data_ptr(), Wp.data.data_ptr(), w_scale.data_ptr(),
                                   0 if bias is None else bias.data_ptr(), T, d_in, d_out, dt, out.data_ptr(), ldy, z,
@@ -788,7 +789,7 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
         n = rows.numel()
         _vector(rows, torch.int32, (n,), "rows")
     out, dt, ldy, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
-    _whole_rows(X)
+    ldx = _whole_rows(X, ldx)
     st = _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
     _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), ldx, x_scale.data_ptr(), x_rows,
                                           0 if rows is None else rows.data_ptr(), n, We.ptrs, w_scale.data_ptr(),

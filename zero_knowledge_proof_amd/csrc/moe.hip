@@ -511,7 +511,8 @@ extern "C" int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, i
   const SortArgs sa{ids, id_bytes == 8, T * K, K, E, 0, 0, offsets, slots, tokens, rows, (int32_t*)ws};
   const RowArgs ra = row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds);
   // few slots in one launch: every workgroup reads all ids for each of its token's choices
-  if (T > 0 && d > 0 && T * K <= SORT_FUSED && K <= 16) return launch_dispatch_few(elem_bytes, sa, ra, stream);
+  if (T > 0 && d > 0 && T * K <= SORT_FUSED && K <= 16 && (int64_t)T * ra.pieces <= (1 << 22))
+    return launch_dispatch_few(elem_bytes, sa, ra, stream);
   rc = launch_sort(sa, stream);
   if (rc || T == 0 || d == 0) return rc;
   return launch_permute(elem_bytes, ra, stream);

@@ -389,14 +389,16 @@ int launch_turns(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_d
 // only the wave itself uses, so the loop has no barrier. (Fragments of X read
 // from memory touch 32 rows a load: 38 us against 19 us for 64 tokens, K =
 // 14336, 4096 outputs.) The waves' sums meet in LDS (integers: any order gives
-// the same), 32 tokens at a time, and a thread finishes one output of each.
+// the same), 32 tokens at a time, and a thread finishes four outputs of a row in
+// the 64-output tiles (one each: 777 tokens of 1008 -> 1003 7.0 us, four 6.0),
+// one in the 32-output ones (one token, 4096 -> 14336: 10.4 us, four 10.9).
 template <int NW, int TM, int XR, int PF, bool GROUPED, bool XV, typename YT>
 __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, GroupPtrs gp) {
   constexpr int NT = NW * 64, TN = (XR + 3) / 4, BT = 8 * XR, BK = WP_BK, UK = 2 * BK, PX = XR <= 4 ? PF : 1;
   constexpr int XP = UK + 16;  // bytes per token of a wave's X
-  constexpr int RP = 36;       // words per token of a wave's sums (both: 16-byte rows in distinct banks)
-  static_assert(32 * XP == 32 * RP * 4, "a wave's sums take the space of 32 tokens");
-  __shared__ __align__(16) int8_t lds[NW * 32 * TN * XP];
+  constexpr int RP = 32 * TM + 4;  // words per token of a wave's sums (both: 16-byte rows in distinct banks)
+  constexpr int XB = NW * 32 * TN * XP, RB = NW * 32 * RP * 4;
+  __shared__ __align__(16) int8_t lds[XB > RB ? XB : RB];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
   int to, t_base, t_lim;
@@ -432,23 +434,25 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
 #pragma unroll
   for (int i = 0; i < TM; ++i) pw[i] = W + (int64_t)min(to * TM + i, a.wp_rb - 1) * NB * (BK * 32);
   const int8_t* px[XR];
-  // the epilogue's scales, read before the products: a thread finishes one
-  // output of every 32 in every (NT / 32)-th token
-  constexpr int TP = NT / 32, MP = (32 + TP - 1) / TP;
-  float ew[TM], eb[TM], exs[TN][MP];
+  // the epilogue's scales, read before the products: a thread finishes OQ
+  // outputs of every TP-th token of 32
+  constexpr int OQ = TM == 1 ? 1 : 4, QR = 32 * TM / OQ, TP = NT / QR, MP = (32 + TP - 1) / TP;
+  const int eq = (tid % QR) * OQ, eo = to * TM * 32 + eq, en = min(a.N - eo, OQ);
+  v4f ew = {0.f, 0.f, 0.f, 0.f}, eb = {0.f, 0.f, 0.f, 0.f};
+  float exs[TN][MP];
   bool elive[TN][MP];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int o = min((to * TM + i) * 32 + (tid & 31), a.N - 1);
-    ew[i] = wsc[o];
-    eb[i] = bias ? bias[o] : 0.f;
-  }
+  for (int q = 0; q < OQ; ++q)
+    if (q < en) {
+      ew[q] = wsc[eo + q];
+      if (bias) eb[q] = bias[eo + q];
+    }
 #pragma unroll
   for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int m = 0; m < MP; ++m) {
-      const int tl = (tid >> 5) + m * TP, x = 32 * j + tl < BT ? x_row(t_base + 32 * j + tl) : -1;
-      elive[j][m] = x >= 0;
+      const int tl = tid / QR + m * TP, x = tl < 32 && 32 * j + tl < BT ? x_row(t_base + 32 * j + tl) : -1;
+      elive[j][m] = x >= 0 && en > 0;
       exs[j][m] = x >= 0 ? a.xs[x] : 0.f;
     }
   const int kc = (lane & 7) * 16;
@@ -521,27 +525,35 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     if (32 * j >= live) break;
+    __syncthreads();  // every wave is done with X, or with the sums of the last 32 tokens
+    if (32 * j + r < live) {
+      int32_t* dst = red + (wave * 32 + r) * RP + 4 * h;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      __syncthreads();  // every wave is done with X, or with the sums of the last block
-      if (32 * j + r < live) {
-        int32_t* dst = red + (wave * 32 + r) * RP + 4 * h;
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *(v4i*)(dst + 8 * g) =
+          *(v4i*)(dst + 32 * i + 8 * g) =
               v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-      }
-      __syncthreads();
+    }
+    __syncthreads();
 #pragma unroll
-      for (int m = 0; m < MP; ++m) {
-        const int tl = (tid >> 5) + m * TP, o = (to * TM + i) * 32 + (tid & 31);
-        if (!elive[j][m] || o >= a.N) continue;
+    for (int m = 0; m < MP; ++m) {
+      const int tl = tid / QR + m * TP;
+      if (!elive[j][m]) continue;
+      const int64_t t = t_base + 32 * j + tl;
+      YT* const y = (YT*)a.Y + t * a.ldy + eo;
+      int32_t* const zp = a.Z ? a.Z + t * a.ldz + eo : nullptr;
+      if constexpr (OQ == 4) {
+        v4i z = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) z += *(const v4i*)&red[(w * 32 + tl) * RP + eq];
+        sdev::store4<YT>(z, exs[j][m], ew, eb, en, y, a.vecY, zp, a.vecZ);
+      } else {
         int32_t z = 0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) z += red[(w * 32 + tl) * RP + (tid & 31)];
-        const int64_t t = t_base + 32 * j + tl;
-        sdev::store_elem((YT*)a.Y + t * a.ldy + o, __builtin_fmaf((float)z * exs[j][m], ew[i], eb[i]));
-        if (a.Z) a.Z[t * a.ldz + o] = z;
+        for (int w = 0; w < NW; ++w) z += red[(w * 32 + tl) * RP + eq];
+        sdev::store_elem(y, __builtin_fmaf((float)z * exs[j][m], ew[0], eb[0]));
+        if (zp) *zp = z;
       }
     }
   }
