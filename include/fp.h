@@ -13,6 +13,10 @@
  * committed remainder r = g^ - 2^k g_w that the matmul's sum-check uses in
  * place of g^; Goldilocks).
  *
+ * Beside the proof, the same layer's answer: the integer product with a scale
+ * for each token and output channel, dense or for tokens grouped by expert, and
+ * the tokens' way to their experts and back (with its gradients).
+ *
  * Conventions (readings where the page is silent):
  *  - rounding ties go up: Q = floor((Z + 2^(s-1)) / 2^s); R = Z - 2^s Q is taken
  *    against the unclamped Q; 1 <= s <= 8 so R fits int8;

@@ -79,7 +79,8 @@ __device__ __forceinline__ void scan_buckets(const int* tot, int B, int* wsum, i
 // Workgroup b places its range: the first row of each bucket from the counts
 // of all ranges (its own alone when there is one), then a round of SORT_NT
 // slots at a time, each lane's rank among its wave's lanes of the same bucket
-// by ballots over the bucket's bits, the waves' counts added in order.
+// by ballots over the bucket's bits, the waves' counts added in order. Bound by
+// latency: 131072 slots in 11 us with the counts' launch.
 __global__ __launch_bounds__(SORT_NT) void sort_place_kernel(SortArgs a) {
   __shared__ int base[MAXB], tot[MAXB];
   __shared__ uint16_t cnt[SORT_NW][MAXB + 1];
@@ -176,7 +177,8 @@ __device__ __forceinline__ void piece_at(int64_t i, int32_t pieces, int64_t& t, 
 }
 
 // Every choice's row a copy of its token's (E: an unsigned type of the
-// elements' size).
+// elements' size). Bound by the copies' bytes (16384 tokens of 8 choices, 4096
+// bf16: 1.21 GB in 205-230 us, 5.2-5.9 TB/s; stores past the caches the same).
 template <typename E>
 __global__ __launch_bounds__(ROW_NT) void permute_kernel(RowArgs a) {
   constexpr int EV = 16 / (int)sizeof(E);
@@ -196,7 +198,8 @@ __global__ __launch_bounds__(ROW_NT) void permute_kernel(RowArgs a) {
 // the slots of its token among all (a slot's row is the number of slots of
 // lower buckets and of earlier ones of its own), so none waits for another;
 // the last workgroup writes the offsets. 256 threads read at most SORT_FUSED
-// ids each from L2. (In two launches one token with 8 choices took 9.2 us.)
+// ids each from L2. One token with 8 choices, 5120 bf16: 4.4 us (the sort and
+// the gather in two launches 9.2).
 template <typename E>
 __global__ __launch_bounds__(ROW_NT) void dispatch_few_kernel(SortArgs s, RowArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;
@@ -323,7 +326,8 @@ constexpr int KG = 4;  // choices whose gradients are made together (eight: 27 u
 
 // A workgroup per token: up to KG choices at a time, each thread's columns of
 // dY read once for them. The dot products' order is fixed: a thread's columns
-// in turn, the lanes of a wave by halves, the waves in order.
+// in turn, the lanes of a wave by halves, the waves in order. Bound by the rows'
+// bytes (8192 tokens of 8 choices, 4096 bf16: 1.14 GB in 212-236 us).
 template <typename E>
 __global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;

@@ -137,12 +137,18 @@ struct ScaleTables {
 // Each K block of 64 bytes is two phases for a wave, a barrier after each: in
 // the first it reads its X fragments from LDS (and stores X of the stage after);
 // in the second it issues its 4 TN products with the loads of later blocks
-// between them. The two groups of waves
-// (the lower and the upper 128 outputs; one wave of each on every SIMD) run
-// one phase apart, so that one wave's products fill the matrix cores while the
+// between them. The two groups of waves (the lower and the upper 128 outputs;
+// one wave of each on every SIMD) run one phase apart, so that one wave's products fill the matrix cores while the
 // other's fragments arrive. The two waves that share weight fragments are in
 // one group, so that the second's loads find the first's in L1. X is staged
 // two blocks (whole 128-byte lines) at a time.
+// Measured: 8192 x 8192 -> 8192 in 441-463 us (2.4-2.5 POP/s), the matrix cores
+// busy 67% of the cycles at a clock that the power limit holds at 1.68 GHz; 4096
+// x 4096 -> 14336 in 226-235 us; 512 tokens of it in 36 us, latency-bound (2.44
+// GHz, busy 24%). Without the alternation (one barrier a stage) 3-7% slower,
+// with raised priority around the products 10%, with waves of 32 outputs x all
+// tokens (no weight fragment loaded twice) 2% slower on large tiles and 3%
+// faster on groups of few rows; weights two or four blocks ahead 2% slower.
 template <int TN>
 struct PCfg {
   static constexpr int NT = 512, BO = 256, BT = 64 * TN, BK = WP_BK, XK = 2 * BK, PITCH = XK + 16, NCB = BT * 8, CB = NCB / NT;
@@ -384,7 +390,8 @@ int launch_turns(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_d
 // ---- few tokens or small products: the K range split over a workgroup -------
 // A tile is 32 TM outputs x 8 XR tokens. The NW waves of its workgroup take units
 // of 128 bytes of K in turn (unit w, w + NW, ...), each into accumulators of
-// its own. Weight fragments go straight into registers; X is read as whole
+// its own. Bound by the weights' bytes for few tokens (one, 4096 -> 14336: 10.4 us,
+// 5.6 TB/s). Weight fragments go straight into registers; X is read as whole
 // lines (8 rows of 128 bytes a load) and turned into fragments through LDS that
 // only the wave itself uses, so the loop has no barrier. (Fragments of X read
 // from memory touch 32 rows a load: 38 us against 19 us for 64 tokens, K =
@@ -577,16 +584,16 @@ int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt
 
 // Which kernel and tile (measured in a graph of calls, weights of three layers
 // in turn; a "block" is 64 bytes of K):
-//  - up to 8 rows: 32 outputs x 8 rows (T = 1, 4096 -> 14336: 10.5 us; with
+//  - up to 8 rows: 32 outputs x 8 rows (T = 1, 4096 -> 14336: 10.4 us; with
 //    tiles of 32 rows 11.0, of 64 x 64 11.8, the turns kernel 23);
 //  - else the row kernel's largest tile that gives most CUs a workgroup: 64 x 64
-//    (T = 200, 4096 -> 4096: 11.3 us, 32 x 32 15.0), 64 x 32 (T = 128, 14336 ->
-//    4096: 19.3 us, 64 x 64 23.8, 32 x 32 23.3), 32 x 32 (T = 64, 14336 -> 4096:
-//    14.2 us, 64 x 32 18.2, 64 x 64 23.6);
+//    (T = 200, 4096 -> 4096: 10.1 us, 32 x 32 15.0), 64 x 32 (T = 128, 14336 ->
+//    4096: 19.0 us, 64 x 64 23.8, 32 x 32 23.3), 32 x 32 (T = 64, 14336 -> 4096:
+//    14.0 us, 64 x 32 18.2, 64 x 64 23.6);
 //  - or the turns kernel where its rounds of tiles cost less: 0.86 us a block
 //    and round of 256-token tiles, 0.5 for the last of 128-token tiles, against
 //    0.115 us a block and 256 tiles of 64 x 64 (T = 512, 4096 -> 14336: 36 us,
-//    64 x 64 53; T = 1000, 2048 -> 2048: 19 us, 64 x 64 13.5).
+//    64 x 64 53; T = 1000, 2048 -> 2048: 19 us, 64 x 64 12.9).
 // Groups: by the rows a group has on average, more than two take the turns
 // kernel (2048 rows in 128 groups, 5120 -> 8192: 0.92 ms, 64 x 64 1.04, 32 x 32
 // 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.7 us, 18.8, 25.3), fewer the
