@@ -82,7 +82,8 @@ def test_sort_agrees_with_the_host_plan(fp):
 
 
 MOVES = [(1, 1, 1, 1), (1, 8, 128, 5120), (3, 2, 4, 7), (65, 3, 7, 96), (300, 6, 60, 1111), (129, 2, 9, 4096), (700, 8, 32, 200), (5, 16, 20, 24),
-         (2, 1, 3, 20000), (1200, 8, 64, 64)]
+         (2, 1, 3, 20000), (1200, 8, 64, 64),
+         (20, 4, 1000, 33), (3, 20, 30, 40), (512, 4, 700, 16)]
 
 
 @pytest.mark.parametrize("T,K,E,d", MOVES)

@@ -80,7 +80,7 @@ def test_scaled_matmul_any_rows(fp, T, d_in, d_out, pad, offset):
 
 
 def test_one_row_at_the_end_of_its_storage(fp):
-    """A single row whose last 16-byte chunk would leave its storage is read byte by byte."""
+    """A single row whose last 16-byte chunk would leave its storage is read to its end only."""
     rng = np.random.default_rng(8)
     _, W, _, ws, _ = inputs(rng, 1, 100, 70)
     buf = torch.from_numpy(rng.integers(-128, 128, size=3 * 128 + 100, dtype=np.int8)).cuda()
@@ -108,6 +108,24 @@ def test_scaled_matmul_strided_out(fp, T, d_out, dt):
         y.fill_(5.0)
         z.fill_(5)
         assert bool((big == 5.0).all()) and bool((zig == 5).all())
+
+
+@pytest.mark.parametrize("T,d_in,d_out,dt", [(1000, 2000, 8000, torch.bfloat16), (900, 1999, 8100, torch.float32),
+                                             (4200, 640, 4200, torch.bfloat16), (2100, 1111, 8200, torch.float16),
+                                             (513, 4096, 14336, torch.bfloat16)])
+def test_large_tiles(fp, T, d_in, d_out, dt):
+    """Products of whole tiles, of half tiles, of both, with ragged last ones in every direction (references by a 64-bit
+    product on the GPU, exact for these integers)."""
+    rng = np.random.default_rng(T + d_out)
+    X, W, xs, ws, bias = inputs(rng, T, d_in, d_out)
+    big = torch.full((T + 2, d_out + 8), 5.0, dtype=dt, device="cuda")
+    z = torch.full((T, d_out), 7, dtype=torch.int32, device="cuda")
+    fp.scaled_matmul(X, xs, fp.pack_weights(W), ws, bias=bias, out=big[1:T + 1, :d_out], Z=z)
+    Z = X.double() @ W.double().t().contiguous()
+    assert torch.equal(z, Z.to(torch.int32))
+    S = Z * xs.double()[:, None] * ws.double()
+    close(big[1:T + 1, :d_out], (S + bias.double()).cpu().numpy(), (S.abs() + bias.double().abs()).cpu().numpy(), dt)
+    assert bool((big[0] == 5.0).all()) and bool((big[T + 1] == 5.0).all()) and bool((big[:, d_out:] == 5.0).all())
 
 
 def test_extremes(fp):
@@ -262,6 +280,24 @@ def test_grouped(fp, counts, x_rows, d_in, d_out, index):
             assert np.array_equal(z[sl].cpu().numpy(), Z.astype(np.int64)), g
             close(y[sl], Y, mag, dt)
         assert bool((y[o[-1]:] == 9.0).all()) and bool((z[o[-1]:] == 9).all())
+
+
+def test_grouped_large_tiles(fp):
+    """Groups of several tiles, of one row and of none, whose last tiles are of every width, over many weight panels."""
+    rng = np.random.default_rng(77)
+    counts = [600, 0, 1, 257, 130, 65, 0, 64, 512, 33]
+    X, xs, W, ws, bias, off, rows, n = group_inputs(rng, counts, 400, 448, 1500, True, 5)
+    y = torch.full((n, 1500), 9.0, dtype=torch.bfloat16, device="cuda")
+    z = torch.full((n, 1500), 9, dtype=torch.int32, device="cuda")
+    fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), ws, off, rows=rows, bias=bias, out=y, Z=z)
+    o = off.tolist()
+    for g, c in enumerate(counts):
+        if c:
+            pick = rows[o[g]:o[g + 1]].long()
+            Z, Y, mag = reference(X[pick], W[g], xs[pick], ws[g], bias[g])
+            assert np.array_equal(z[o[g]:o[g + 1]].cpu().numpy(), Z.astype(np.int64)), g
+            close(y[o[g]:o[g + 1]], Y, mag, torch.bfloat16)
+    assert bool((y[o[-1]:] == 9.0).all()) and bool((z[o[-1]:] == 9).all())
 
 
 def test_grouped_unaligned_and_index_out_of_range(fp):

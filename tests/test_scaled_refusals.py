@@ -138,7 +138,7 @@ def test_binding():
     if s.data_ptr() % 16 == 0:
         with pytest.raises(ValueError, match="storage"):
             fp._whole_rows(torch.as_strided(s, (3, 20), (32, 1)), 32)
-        assert fp._whole_rows(torch.as_strided(s, (1, 20), (32, 1), 64), 32) == 20  # one row: byte by byte instead
+        assert fp._whole_rows(torch.as_strided(s, (1, 20), (32, 1), 64), 32) == 20  # one row: to its end only
         assert fp._whole_rows(torch.as_strided(s, (2, 20), (32, 1)), 32) == 32
     assert fp._whole_rows(torch.zeros(3, 32, dtype=torch.int8)[:, :20], 32) == 32
 

@@ -660,7 +660,7 @@ def _here(*tensors) -> int:
 
 def _whole_rows(X, ld: int) -> int:
     """X's rows, when they start on 16 bytes, are read in whole 16-byte chunks: the last row's must be in its storage.
-    Returns the leading dimension to pass: a single row without the bytes for its last chunk is read byte by byte."""
+    Returns the leading dimension to pass: a single row without the bytes for its last chunk is read to its end only."""
     T, d = X.shape
     up = (d + 15) // 16 * 16
     if up != d and T and ld >= up and ld % 16 == 0 and X.data_ptr() % 16 == 0:

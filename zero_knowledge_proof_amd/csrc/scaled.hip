@@ -138,10 +138,11 @@ struct ScaleTables {
 // the first it reads its X fragments from LDS (and stores X of the stage after);
 // in the second it issues its 4 TN products with the loads of later blocks
 // between them. The two groups of waves (the lower and the upper 128 outputs;
-// one wave of each on every SIMD) run one phase apart, so that one wave's products fill the matrix cores while the
-// other's fragments arrive. The two waves that share weight fragments are in
-// one group, so that the second's loads find the first's in L1. X is staged
-// two blocks (whole 128-byte lines) at a time.
+// one wave of each on every SIMD) run one phase apart, so that one wave's
+// products fill the matrix cores while the other's fragments arrive. The two
+// waves that share weight fragments are in one group, so that the second's
+// loads find the first's in L1. X is staged two blocks (whole 128-byte lines)
+// at a time.
 // Measured: 8192 x 8192 -> 8192 in 441-463 us (2.4-2.5 POP/s), the matrix cores
 // busy 67% of the cycles at a clock that the power limit holds at 1.68 GHz; 4096
 // x 4096 -> 14336 in 226-235 us; 512 tokens of it in 36 us, latency-bound (2.44
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
 #pragma unroll
     for (int c = 0; c < XR; ++c) {
       if constexpr (XV) xr[slot][c] = *(const v4i*)(px[c] + (k < a.K ? k : 0));
-      else xr[slot][c] = load16(px[c], k, a.K, false);
+      else xr[slot][c] = sdev::load16u((const uint8_t*)px[c] + k, a.K - k);
     }
   };
   v16i acc[TM][TN];
@@ -598,8 +599,8 @@ int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt
 // kernel (2048 rows in 128 groups, 5120 -> 8192: 0.92 ms, 64 x 64 1.04, 32 x 32
 // 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.7 us, 18.8, 25.3), fewer the
 // 8-row tiles (16 rows in 16 groups, 4096 -> 14336: 114 us; turns 133).
-// Rows of X that are not whole 16-byte chunks are gathered a byte at a time in
-// 8-row or 64 x 64 tiles.
+// Rows of X that are not whole 16-byte chunks are read at whatever address they
+// have (the last bytes one by one) in 8-row or 64 x 64 tiles.
 template <bool GROUPED, bool XV>
 int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
   if constexpr (GROUPED) {
@@ -626,8 +627,9 @@ int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_d
 int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
 
 // What the product calls share: sizes, pointers, and how X may be read.
-int check_product(const char* fn, const void* X, int64_t ldx, const float* x_scale, const float* w_scale, const float* bias, int32_t T,
-                  int32_t d_in, int32_t d_out, fp_dtype y_dt, const void* Y, int64_t ldy, const int32_t* Z, int64_t ldz) {
+int check_product(const char* fn, const void* X, int64_t ldx, const float* x_scale, const float* w_scale,
+                  const float* bias, int32_t T, int32_t d_in, int32_t d_out, fp_dtype y_dt, const void* Y, int64_t ldy,
+                  const int32_t* Z, int64_t ldz) {
   if (T < 0 || d_in < 0 || d_out < 0) return fpi::fail(FP_EARG, "%s: negative size", fn);
   if (!elem_bytes(y_dt)) return fpi::fail(FP_EARG, "%s: unknown output type %d", fn, (int)y_dt);
   if (d_in > FP_MAX_DIN) return fpi::fail(FP_ESHAPE, "%s: d_in=%d > %d", fn, d_in, FP_MAX_DIN);
