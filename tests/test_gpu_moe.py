@@ -148,6 +148,30 @@ def test_combine_and_gradients(fp, T, K, E, d, dt):
         assert bool((buf == 9.0).all())
 
 
+def test_rows_past_32_bits(fp):
+    """Sorted rows that start more than 2^31 elements into their tensor, there and back."""
+    T, K, E, d = 270000, 2, 16, 4096  # Xs: 2.2 G elements
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    X = torch.randn((T, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((T, K), generator=g, device="cuda")
+    Xs, plan = fp.moe_dispatch(X, ids, E)
+    at = torch.cat([torch.arange(0, 50), torch.arange(T * K - 50, T * K), torch.randint(0, T * K, (200,))]).cuda()
+    assert torch.equal(Xs[at], X[plan.tokens[at].long()])
+    Y = fp.moe_combine(Xs, plan, w)          # both choices hold the token's own row
+    t = torch.cat([torch.arange(0, 20), torch.arange(T - 20, T)]).cuda()
+    x64, w64 = X[t].double().cpu().numpy(), w[t].double().cpu().numpy()
+    terms = w64[:, :, None] * x64[:, None, :]
+    within(Y[t], terms.sum(1), 1.01 * K * U * np.abs(terms).sum(1), torch.bfloat16)
+    dO, dw = fp.moe_combine_backward(X, Xs, plan, w)
+    rows = plan.rows[t].long()
+    for k in range(K):
+        want = w64[:, k, None] * x64
+        within(dO[rows[:, k]], want, U * np.abs(want), torch.bfloat16)
+        within(dw[t, k], (x64 * x64).sum(1), 1.01 * d * U * (x64 * x64).sum(1), torch.float32)
+
+
 def test_combine_infinities_and_no_rows(fp):
     """An infinity or a NaN stays with the tokens that have its row; a weight of zero does not hide a NaN; tokens whose
     slots all were dropped get zeros."""

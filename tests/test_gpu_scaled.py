@@ -128,6 +128,32 @@ def test_large_tiles(fp, T, d_in, d_out, dt):
     assert bool((big[0] == 5.0).all()) and bool((big[T + 1] == 5.0).all()) and bool((big[:, d_out:] == 5.0).all())
 
 
+def test_rows_past_32_bits(fp):
+    """Rows of X, Y and Z that start more than 2^31 bytes (and elements) into their tensors: the last rows equal those of
+    a call on them alone, which takes another kernel."""
+    T, d_in, d_out = 540000, 4096, 4100  # X: 2.2 G bytes; Y: 2.2 G elements
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    X = torch.randint(-128, 128, (T, d_in), generator=g, device="cuda", dtype=torch.int8)
+    W = torch.randint(-128, 128, (d_out, d_in), generator=g, device="cuda", dtype=torch.int8)
+    xs, ws = torch.rand(T, generator=g, device="cuda"), torch.rand(d_out, generator=g, device="cuda")
+    Wp = fp.pack_weights(W)
+    y, z = torch.zeros((T, d_out), dtype=torch.bfloat16, device="cuda"), torch.zeros((T, d_out), dtype=torch.int32, device="cuda")
+    fp.scaled_matmul(X, xs, Wp, ws, out=y, Z=z)
+    for a, b in ((T - 5, T), (262000, 262007), (0, 8)):
+        z2 = torch.zeros((b - a, d_out), dtype=torch.int32, device="cuda")
+        y2 = fp.scaled_matmul(X[a:b], xs[a:b], Wp, ws, Z=z2)
+        assert torch.equal(y[a:b], y2) and torch.equal(z[a:b], z2)
+    # the same rows picked by index for a group, and quantized
+    rows = torch.tensor([T - 1, 0, T - 2], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    y3 = fp.scaled_matmul_grouped(X, xs, fp.PackedExperts([Wp]), ws[None], off, rows=rows)
+    assert torch.equal(y3, y[rows.long()])
+    q, s = fp.quantize_rows(y)
+    q2, s2 = fp.quantize_rows(y[T - 3:].clone())
+    assert torch.equal(q[T - 3:], q2) and torch.equal(s[T - 3:], s2)
+
+
 def test_extremes(fp):
     """The largest |Z| (every product (-128)^2 over d_in = 131071), zero scales, infinities and NaN in the scales, and
     values beyond fp16."""
