@@ -132,45 +132,48 @@ struct ScaleTables {
 };
 
 // ---- large products: two groups of four waves in turn ----------------------
-// A workgroup of eight waves makes a tile of 256 outputs x 64 TN tokens, four
-// waves along the outputs (64 each) and two along the tokens (32 TN each).
-// Each K block of 64 bytes is two phases for a wave, a barrier after each: in
-// the first it reads its X fragments from LDS (and stores X of the stage after);
-// in the second it issues its 4 TN products with the loads of later blocks
-// between them. The two groups of waves (the lower and the upper 128 outputs;
-// one wave of each on every SIMD) run one phase apart, so that one wave's
-// products fill the matrix cores while the other's fragments arrive. The two
-// waves that share weight fragments are in one group, so that the second's
-// loads find the first's in L1. X is staged two blocks (whole 128-byte lines)
-// at a time.
+// A workgroup of eight waves makes a tile of 256 outputs: of 256 tokens with
+// waves of 64 outputs x 128 tokens (TM = 2, TN = 4), of 128 or 64 tokens with
+// waves of 32 outputs x all of them (TM = 1, TN = 4 or 2). Each K block of 64
+// bytes is two phases for a wave, a barrier after each: in the first it reads
+// its X fragments from LDS (and stores X of the stage after); in the second it
+// issues its 2 TM TN products with the loads of later blocks between them. The
+// two groups of waves (the lower and the upper 128 outputs; one wave of each on
+// every SIMD) run one phase apart, so that one wave's products fill the matrix
+// cores while the other's fragments arrive. Where two waves share weight
+// fragments they are in one group, so that the second's loads find the first's
+// in L1. X is staged two blocks (whole 128-byte lines) at a time.
 // Measured: 8192 x 8192 -> 8192 in 441-463 us (2.4-2.5 POP/s), the matrix cores
 // busy 67% of the cycles at a clock that the power limit holds at 1.68 GHz; 4096
 // x 4096 -> 14336 in 226-235 us; 512 tokens of it in 36 us, latency-bound (2.44
 // GHz, busy 24%). Without the alternation (one barrier a stage) 3-7% slower,
-// with raised priority around the products 10%, with waves of 32 outputs x all
-// tokens (no weight fragment loaded twice) 2% slower on large tiles and 3%
-// faster on groups of few rows; weights two or four blocks ahead 2% slower.
-template <int TN>
+// with raised priority around the products 10%; weights two or four blocks ahead
+// 2% slower. Waves of 32 outputs x all tokens, which load no weight fragment
+// twice but read twice as much X from LDS: 2% slower for 256 tokens, the same or
+// faster below (2048 rows in 128 groups, 5120 -> 8192: 923 -> 904 us; 128 rows in
+// 16 groups, 4096 -> 14336: 190 -> 183).
+template <int TM, int TN>
 struct PCfg {
-  static constexpr int NT = 512, BO = 256, BT = 64 * TN, BK = WP_BK, XK = 2 * BK, PITCH = XK + 16, NCB = BT * 8, CB = NCB / NT;
-  static constexpr int EP = 68;  // words per token of a wave's 64 outputs in the epilogue
+  static constexpr int NT = 512, BO = 256, BT = 32 * TM * TN, BK = WP_BK, XK = 2 * BK, PITCH = XK + 16, NCB = BT * 8, CB = NCB / NT;
+  static constexpr int EP = 32 * TM + 4;  // words per token of a wave's outputs in the epilogue
   static constexpr int LDS_BYTES = 2 * BT * PITCH;
   static_assert(NCB % NT == 0, "X chunks: whole rounds");
-  static_assert(TN < 4 || LDS_BYTES >= 8 * 32 * EP * 4, "the epilogue's rows fit the widest tile's stages");
+  static_assert(TM < 2 || TN < 4 || LDS_BYTES >= 8 * 32 * EP * 4, "the epilogue's rows fit the widest tile's stages");
 };
 
-// The tile of outputs o_base.. and tokens [t_base, t_lim) (at most 64 TN).
-template <int TN, bool GROUPED, typename YT>
+// The tile of outputs o_base.. and tokens [t_base, t_lim) (at most 32 TM TN).
+template <int TM, int TN, bool GROUPED, typename YT>
 __device__ __forceinline__ void turns_body(const ScaledArgs& a, const int8_t* W, const float* wsc, const float* bias,
                                            int o_base, int t_base, int t_lim, int8_t* lds) {
-  using C = PCfg<TN>;
-  constexpr int NT = C::NT, BT = C::BT, BK = C::BK, PITCH = C::PITCH, CB = C::CB, TM = 2, KS = 2;
+  using C = PCfg<TM, TN>;
+  constexpr int NT = C::NT, BT = C::BT, BK = C::BK, PITCH = C::PITCH, CB = C::CB, KS = 2;
   constexpr int PFW = 3, U = 12;  // weight blocks in registers; steps after which slots and stages repeat
-  ScaleTables& tab = *reinterpret_cast<ScaleTables*>(lds + PCfg<4>::LDS_BYTES);
+  ScaleTables& tab = *reinterpret_cast<ScaleTables*>(lds + PCfg<2, 4>::LDS_BYTES);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
   const int group = wave >> 2;
-  const int wo0 = (wave >> 2) * 128 + (wave & 1) * 64, wt0 = ((wave >> 1) & 1) * 32 * TN;
+  const int wo0 = TM == 2 ? group * 128 + (wave & 1) * 64 : wave * 32;
+  const int wt0 = TM == 2 ? ((wave >> 1) & 1) * 32 * TN : 0;
   auto x_row = [&](int t) -> int {
     if (t >= t_lim) return -1;
     if (!GROUPED || !a.rows) return t;
@@ -276,10 +279,11 @@ __device__ __forceinline__ void turns_body(const ScaledArgs& a, const int8_t* W,
     if (!group) turn();  // as many barriers as the second group
   }
   // ---- epilogue: each wave's products pass through LDS 32 tokens at a time,
-  // so that 16 lanes store a row's 64 outputs (128 bytes of bf16) together
+  // so that 8 TM lanes store a row's 32 TM outputs together
   __syncthreads();  // every wave is done with X, and the tables are written
   int32_t* E = reinterpret_cast<int32_t*>(lds) + wave * 32 * C::EP;
-  const int ol = wo0 + (lane & 15) * 4, o0 = o_base + ol, nv = min(a.N - o0, 4);
+  constexpr int LR = 8 * TM, RI = 64 / LR;  // lanes to a row, rows at a time
+  const int ol = wo0 + (lane % LR) * 4, o0 = o_base + ol, nv = min(a.N - o0, 4);
   const v4f w4 = *(const v4f*)&tab.ws[ol], b4 = *(const v4f*)&tab.bias[ol];
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
@@ -291,9 +295,9 @@ __device__ __forceinline__ void turns_body(const ScaledArgs& a, const int8_t* W,
             v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 2
-    for (int p = 0; p < 8; ++p) {
-      const int row = 4 * p + (lane >> 4), tl = wt0 + 32 * j + row;
-      const v4i z = *(const v4i*)&E[row * C::EP + (lane & 15) * 4];
+    for (int p = 0; p < 32 / RI; ++p) {
+      const int row = RI * p + lane / LR, tl = wt0 + 32 * j + row;
+      const v4i z = *(const v4i*)&E[row * C::EP + (lane % LR) * 4];
       if (tab.row[tl] < 0 || nv <= 0) continue;
       const int64_t t = t_base + tl;
       sdev::store4<YT>(z, tab.xs[tl], w4, b4, nv, (YT*)a.Y + t * a.ldy + o0, a.vecY, a.Z ? a.Z + t * a.ldz + o0 : nullptr,
@@ -309,7 +313,7 @@ __device__ __forceinline__ void turns_body(const ScaledArgs& a, const int8_t* W,
 // tiles end with their groups. A tile of few rows takes a narrower body.
 template <bool GROUPED, typename YT>
 __global__ __launch_bounds__(512, 2) void scaled_turns_kernel(ScaledArgs a, GroupPtrs gp) {
-  __shared__ __align__(16) int8_t lds[PCfg<4>::LDS_BYTES + sizeof(ScaleTables)];
+  __shared__ __align__(16) int8_t lds[PCfg<2, 4>::LDS_BYTES + sizeof(ScaleTables)];
   const int8_t* W = a.W;
   const float* wsc = a.ws;
   const float* bias = a.bias;
@@ -356,9 +360,9 @@ __global__ __launch_bounds__(512, 2) void scaled_turns_kernel(ScaledArgs a, Grou
     }
   }
   const int live = t_lim - t_base;
-  if (live > 128) turns_body<4, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
-  else if (live > 64) turns_body<2, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
-  else turns_body<1, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+  if (live > 128) turns_body<2, 4, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+  else if (live > 64) turns_body<1, 4, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
+  else turns_body<1, 2, GROUPED, YT>(a, W, wsc, bias, o_base, t_base, t_lim, lds);
 }
 
 // Of these tiles of 256 tokens, how many are made whole.
@@ -596,8 +600,8 @@ int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt
 //    0.115 us a block and 256 tiles of 64 x 64 (T = 512, 4096 -> 14336: 36 us,
 //    64 x 64 53; T = 1000, 2048 -> 2048: 19 us, 64 x 64 12.9).
 // Groups: by the rows a group has on average, more than two take the turns
-// kernel (2048 rows in 128 groups, 5120 -> 8192: 0.92 ms, 64 x 64 1.04, 32 x 32
-// 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.7 us, 18.8, 25.3), fewer the
+// kernel (2048 rows in 128 groups, 5120 -> 8192: 0.90 ms, 64 x 64 1.04, 32 x 32
+// 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.1 us, 18.8, 25.3), fewer the
 // 8-row tiles (16 rows in 16 groups, 4096 -> 14336: 114 us; turns 133).
 // Rows of X that are not whole 16-byte chunks are read at whatever address they
 // have (the last bytes one by one) in 8-row or 64 x 64 tiles (777 rows of 1000
