@@ -170,7 +170,7 @@ size_t fp_moe_sort_workspace(int32_t T, int32_t K, int32_t E);
 /* Xs[rows[t, k], :] = X[t, :] for every slot with a row in [0, T K): the
  * tokens' rows in sorted order. Elements of 1, 2 or 4 bytes, d to a row; X
  * [T, d] (leading dim ldx), Xs [T K, d] (lds). Rows of Xs that no slot has are
- * left as they were. */
+ * left as they were. A row, here and below, is of at most 2^31 - 16 bytes. */
 int fp_moe_permute(int32_t elem_bytes, const void* X, int64_t ldx, int32_t T, int32_t K, int32_t d,
                    const int32_t* rows, void* Xs, int64_t lds, hipStream_t stream);
 
@@ -190,8 +190,9 @@ int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n_rows, cons
 /* The gradients of fp_moe_combine from dY [T, d] (lddy): dO[rows[t, k], :] =
  * w[t, k] dY[t, :] (rows of dO that no slot has are left as they were; the
  * rows must be distinct, as fp_moe_sort writes them) and dw[t, k] =
- * <dY[t, :], O[rows[t, k], :]> (device fp32 [T, K] dense, summed in fp32 in a
- * fixed order; 0 for a slot without a row). */
+ * <dY[t, :], O[rows[t, k], :]> (device fp32 [T, K] dense, summed in fp32 in an
+ * order fixed by d, the type and what the addresses and leading dimensions are
+ * whole in: 16 bytes, 4 or 2; 0 for a slot without a row). */
 int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const void* O, int64_t ldo, int32_t n_rows,
                             const int32_t* rows, const float* w, int32_t T, int32_t K, int32_t d, void* dO,
                             int64_t lddo, float* dw, hipStream_t stream);

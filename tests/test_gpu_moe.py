@@ -107,6 +107,24 @@ def test_dispatch(fp, T, K, E, d, dt):
         assert bool((out == 9).all())
 
 
+@pytest.mark.parametrize("T,K", [(6, 3), (1100, 4)])
+@pytest.mark.parametrize("d,pad", [(1, 0), (2, 0), (3, 0), (1023, 0), (1025, 0), (4098, 0), (4103, 0), (2052, 4), (4111, 1), (8210, 2)])
+@pytest.mark.parametrize("dt", [torch.int8, torch.bfloat16])
+def test_rows_of_every_length(fp, T, K, d, pad, dt):
+    """Rows that end in each part of a word, over several pieces, in both launches."""
+    E = 7
+    rng = np.random.default_rng(d + T)
+    ids = draw_ids(rng, T, K, E, "wild")
+    _, slots, _ = sorted_slots(ids, E)
+    X = torch.from_numpy(rng.integers(-128, 128, (T, d + pad), dtype=np.int8)).cuda().to(dt)[:, :d]
+    out = torch.full((T * K, d + pad), 99, dtype=dt, device="cuda")
+    fp.moe_dispatch(X, torch.from_numpy(ids).cuda(), E, out=out[:, :d])
+    want = torch.full((T * K, d + pad), 99, dtype=dt, device="cuda")
+    live = torch.from_numpy(slots >= 0).cuda()
+    want[live, :d] = X[torch.from_numpy(slots[slots >= 0] // K).cuda()]
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("T,K,E,d", MOVES)
 @pytest.mark.parametrize("dt", TYPES)
 def test_combine_and_gradients(fp, T, K, E, d, dt):

@@ -103,6 +103,16 @@ def test_moe_rows():
     assert bwd(dO=ODD) == EARG and bwd(n=-1) == EARG
 
 
+def test_moe_rows_of_2_31_bytes():
+    L, d = fp.lib(), 1 << 30
+    assert L.fp_moe_permute(2, D, d, 2, 2, d, D, D, d, None) == ESHAPE
+    assert L.fp_moe_combine(BF16, D, d, 4, D, None, 2, 2, d, D, d, None) == ESHAPE
+    assert L.fp_moe_combine_backward(F32, D, d, D, d, 4, D, D, 2, 2, d, D, d, D, None) == ESHAPE
+    ok = (1 << 31) - 16  # the widest row
+    assert L.fp_moe_permute(1, None, ok, 0, 2, ok, None, None, ok, None) == 0
+    assert L.fp_moe_permute(1, None, ok + 1, 0, 2, ok + 1, None, None, ok + 1, None) == ESHAPE
+
+
 def test_binding():
     """Shapes, types and strides are checked before anything reaches the device."""
     Wp = fp.PackedWeights(torch.zeros(64 * 64, dtype=torch.int8), 40, 64)

@@ -9,9 +9,8 @@
 //   gradients dX[t] = sum_k dXs[rows[t, k]]
 //             dO[rows[t, k]] = w[t, k] dY[t],  dw[t, k] = <dY[t], O[rows[t, k]]>
 // All but the sort are bound by the rows they move: each is read and written
-// once, a piece of a token's row (a 16-byte load a lane, at whatever address the
-// row has) by one workgroup for all of the token's choices, whose rows are all
-// asked for before the first arrives.
+// once, a piece of a token's row (16 bytes a lane) by one wave for all of the
+// token's choices, whose rows are asked for several at a time.
 #include "common.hpp"
 #include "scaled_dev.hpp"
 
@@ -160,36 +159,42 @@ constexpr int ROW_NT = 256;
 constexpr int KC = 8;  // choices that a token's workgroup ranks together
 
 struct RowArgs {
-  const void* X;
-  int64_t ldx;
-  void* Xs;
+  const char* X;
+  int64_t ldx;  // bytes, as lds
+  char* Xs;
   int64_t lds;
   const int32_t* rows;  // [T, K]
-  int32_t T, K, n_rows, d;
-  int32_t pieces;  // of a row, ROW_NT 16-byte units each
+  int32_t T, K, n_rows;
+  uint32_t bytes;  // of a row
+  int32_t pieces;  // of a row, 16 bytes a lane each (a wave's, or a workgroup's in the fused launch)
 };
 
-// Piece i of the launch: token t = i / pieces, columns c0.. of this thread.
-template <int EV>
-__device__ __forceinline__ void piece_at(int64_t i, int32_t pieces, int64_t& t, int64_t& c) {
+// Wave task i of a launch: token t = i / pieces, this lane's first unit.
+template <int UB>
+__device__ __forceinline__ void wave_piece(int64_t i, int32_t pieces, int64_t& t, uint32_t& at) {
   t = i / pieces;
-  c = ((i - t * pieces) * ROW_NT + threadIdx.x) * EV;
+  at = (uint32_t)(i - t * pieces) * (64 * 16 / sdev::unit_size<UB>()) + (threadIdx.x & 63);
 }
+// The wave's first task and the tasks of the launch's waves.
+__device__ __forceinline__ int64_t first_task() {
+  return (int64_t)blockIdx.x * (ROW_NT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+__device__ __forceinline__ int64_t task_step() { return (int64_t)gridDim.x * (ROW_NT / 64); }
 
-// Every choice's row a copy of its token's (E: an unsigned type of the
-// elements' size). Bound by the copies' bytes (16384 tokens of 8 choices, 4096
-// bf16: 1.21 GB in 205-230 us, 5.2-5.9 TB/s; stores past the caches the same).
-template <typename E>
+// Every choice's row a copy of its token's. Bound by the copies' bytes (16384
+// tokens of 8 choices, 4096 bf16: 1.21 GB in 205-233 us, 5.2-5.9 TB/s; stores
+// past the caches the same; 10000 tokens of 6 choices in rows of 4445 bytes: 311
+// MB in 78 us, of 4096 bytes 58).
+template <int UB>
 __global__ __launch_bounds__(ROW_NT) void permute_kernel(RowArgs a) {
-  constexpr int EV = 16 / (int)sizeof(E);
-  for (int64_t i = blockIdx.x; i < (int64_t)a.T * a.pieces; i += gridDim.x) {
-    int64_t t, c;
-    piece_at<EV>(i, a.pieces, t, c);
-    if (c >= a.d) continue;
-    const v4i v = sdev::load16u((const E*)a.X + t * a.ldx + c, a.d - c);
+  for (int64_t i = first_task(); i < (int64_t)a.T * a.pieces; i += task_step()) {
+    int64_t t;
+    uint32_t at;
+    wave_piece<UB>(i, a.pieces, t, at);
+    const v4i v = sdev::load_units<UB>(a.X + t * a.ldx, at, 64, a.bytes);
     for (int k = 0; k < a.K; ++k) {
       const int r = a.rows[t * a.K + k];
-      if ((uint32_t)r < (uint32_t)a.n_rows) sdev::store16u((E*)a.Xs + r * a.lds + c, v, a.d - c);
+      if ((uint32_t)r < (uint32_t)a.n_rows) sdev::store_units<UB>(a.Xs + r * a.lds, v, at, 64, a.bytes);
     }
   }
 }
@@ -200,9 +205,9 @@ __global__ __launch_bounds__(ROW_NT) void permute_kernel(RowArgs a) {
 // the last workgroup writes the offsets. 256 threads read at most SORT_FUSED
 // ids each from L2. One token with 8 choices, 5120 bf16: 4.4 us (the sort and
 // the gather in two launches 9.2).
-template <typename E>
+template <int UB>
 __global__ __launch_bounds__(ROW_NT) void dispatch_few_kernel(SortArgs s, RowArgs a) {
-  constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;
+  constexpr int NW = ROW_NT / 64;
   __shared__ int tot[MAXB], wsum[NW], pos[NW][KC];
   __shared__ uint16_t key[SORT_FUSED];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = s.E + 1;
@@ -224,11 +229,10 @@ __global__ __launch_bounds__(ROW_NT) void dispatch_few_kernel(SortArgs s, RowArg
     }
     return;
   }
-  int64_t t, c;
-  piece_at<EV>(blockIdx.x, a.pieces, t, c);
+  const int64_t t = blockIdx.x / a.pieces;
+  const uint32_t at = (blockIdx.x % a.pieces) * (ROW_NT * 16 / sdev::unit_size<UB>()) + tid;
   const bool writes = blockIdx.x % a.pieces == 0;  // the token's first piece writes its slots
-  v4i v = {0, 0, 0, 0};
-  if (c < a.d) v = sdev::load16u((const E*)a.X + t * a.ldx + c, a.d - c);
+  const v4i v = sdev::load_units<UB>(a.X + t * a.ldx, at, ROW_NT, a.bytes);
   for (int j = tid; j < s.N; j += ROW_NT) key[j] = (uint16_t)bucket(s, j);
   __syncthreads();
   for (int k0 = 0; k0 < a.K; k0 += KC) {
@@ -259,31 +263,32 @@ __global__ __launch_bounds__(ROW_NT) void dispatch_few_kernel(SortArgs s, RowArg
         s.tokens[r] = has ? (int)t : -1;
         s.rows[me + k] = has ? r : -1;
       }
-      if (has && c < a.d) sdev::store16u((E*)a.Xs + r * a.lds + c, v, a.d - c);
+      if (has) sdev::store_units<UB>(a.Xs + r * a.lds, v, at, ROW_NT, a.bytes);
     }
   }
 }
 
 struct CombineArgs {
-  const void* O;
-  int64_t ldo;
+  const char* O;
+  int64_t ldo;  // bytes, as ldy
   const int32_t* rows;
   const float* w;  // NULL: all one
-  int32_t T, K, n_rows, d, pieces;
-  void* Y;
+  int32_t T, K, n_rows, pieces;
+  uint32_t bytes;  // of a row
+  char* Y;
   int64_t ldy;
 };
 
 // F rows in flight together: all eight of a few tokens, whose latency counts,
 // four of many (16384 tokens of 8 choices, 4096 bf16: 236 us, with eight 256:
 // more scattered rows are open in memory at once than it serves well).
-template <typename E, int F>
+template <typename E, int UB, int F>
 __global__ __launch_bounds__(ROW_NT) void combine_kernel(CombineArgs a) {
   constexpr int EV = 16 / (int)sizeof(E);
-  for (int64_t i = blockIdx.x; i < (int64_t)a.T * a.pieces; i += gridDim.x) {
-    int64_t t, c;
-    piece_at<EV>(i, a.pieces, t, c);
-    if (c >= a.d) continue;
+  for (int64_t i = first_task(); i < (int64_t)a.T * a.pieces; i += task_step()) {
+    int64_t t;
+    uint32_t at;
+    wave_piece<UB>(i, a.pieces, t, at);
     float y[EV] = {};
     for (int k0 = 0; k0 < a.K; k0 += F) {
       v4i raw[F];
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(ROW_NT) void combine_kernel(CombineArgs a) {
           const int r = a.rows[t * a.K + k0 + k];
           if ((uint32_t)r < (uint32_t)a.n_rows) {
             w[k] = a.w ? a.w[t * a.K + k0 + k] : 1.f;
-            raw[k] = sdev::load16u((const E*)a.O + r * a.ldo + c, a.d - c);
+            raw[k] = sdev::load_units<UB>(a.O + r * a.ldo, at, 64, a.bytes);
           }
         }
       }
@@ -305,19 +310,20 @@ __global__ __launch_bounds__(ROW_NT) void combine_kernel(CombineArgs a) {
 #pragma unroll
         for (int e = 0; e < EV; ++e) y[e] = __builtin_fmaf(w[k], sdev::load_elem<E>(raw[k], e), y[e]);
     }
-    sdev::store16u((E*)a.Y + t * a.ldy + c, sdev::pack16<E>(y), a.d - c);
+    sdev::store_units<UB>(a.Y + t * a.ldy, sdev::pack16<E>(y), at, 64, a.bytes);
   }
 }
 
 struct CombineBwdArgs {
-  const void* dY;
-  int64_t lddy;
-  const void* O;
+  const char* dY;
+  int64_t lddy;  // bytes, as ldo, lddo
+  const char* O;
   int64_t ldo;
   const int32_t* rows;
   const float* w;
-  int32_t T, K, n_rows, d;
-  void* dO;
+  int32_t T, K, n_rows;
+  uint32_t bytes;  // of a row
+  char* dO;
   int64_t lddo;
   float* dw;
 };
@@ -328,13 +334,13 @@ constexpr int KG = 4;  // choices whose gradients are made together (eight: 27 u
 // dY read once for them. The dot products' order is fixed: a thread's columns
 // in turn, the lanes of a wave by halves, the waves in order. Bound by the rows'
 // bytes (8192 tokens of 8 choices, 4096 bf16: 1.14 GB in 212-236 us).
-template <typename E>
+template <typename E, int UB>
 __global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), NW = ROW_NT / 64;
   __shared__ float red[NW][KG];
   const int tid = threadIdx.x;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const E* dy = (const E*)a.dY + t * a.lddy;
+    const char* dy = a.dY + t * a.lddy;
     for (int k0 = 0; k0 < a.K; k0 += KG) {
       int r[KG];
       float w[KG], dot[KG];
@@ -344,12 +350,12 @@ __global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs
         w[k] = k0 + k < a.K ? a.w[t * a.K + k0 + k] : 0.f;
         dot[k] = 0.f;
       }
-      for (int64_t c = tid * EV; c < a.d; c += ROW_NT * EV) {
-        const v4i ry = sdev::load16u(dy + c, a.d - c);
+      for (uint32_t at = tid; at * sdev::unit_size<UB>() < a.bytes; at += ROW_NT * 16 / sdev::unit_size<UB>()) {
+        const v4i ry = sdev::load_units<UB>(dy, at, ROW_NT, a.bytes);
         v4i ro[KG];
 #pragma unroll
         for (int k = 0; k < KG; ++k)
-          if ((uint32_t)r[k] < (uint32_t)a.n_rows) ro[k] = sdev::load16u((const E*)a.O + r[k] * a.ldo + c, a.d - c);
+          if ((uint32_t)r[k] < (uint32_t)a.n_rows) ro[k] = sdev::load_units<UB>(a.O + r[k] * a.ldo, at, ROW_NT, a.bytes);
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
           if ((uint32_t)r[k] >= (uint32_t)a.n_rows) continue;  // uniform
@@ -360,7 +366,7 @@ __global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs
             dot[k] = __builtin_fmaf(y, sdev::load_elem<E>(ro[k], e), dot[k]);
             v[e] = w[k] * y;
           }
-          sdev::store16u((E*)a.dO + r[k] * a.lddo + c, sdev::pack16<E>(v), a.d - c);
+          sdev::store_units<UB>(a.dO + r[k] * a.lddo, sdev::pack16<E>(v), at, ROW_NT, a.bytes);
         }
       }
 #pragma unroll
@@ -402,37 +408,67 @@ void sort_plan(int64_t N, int32_t* nblk, int32_t* per) {
   *nblk = (int32_t)((N + *per - 1) / *per);
 }
 
-// Pieces of a row of d elements of eb bytes, and workgroups for T tokens.
-int32_t row_pieces(int32_t d, int eb) {
-  const int64_t per = (int64_t)ROW_NT * 16 / eb;
-  return (int32_t)((d + per - 1) / per);
-}
-unsigned piece_grid(int32_t T, int32_t pieces) {
-  const int64_t n = (int64_t)T * pieces;
+// What addresses, strides and lengths (their bits in `all`) are whole in, for
+// elements of eb bytes.
+int unit_bytes(uint64_t all, int eb) { return all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : (eb == 1 ? 1 : 2)); }
+
+// Pieces of a row, 16 bytes for each of nt lanes.
+int32_t row_pieces(int64_t bytes, int nt) { return (int32_t)((bytes + nt * 16 - 1) / (nt * 16)); }
+unsigned task_grid(int64_t tasks) {
+  const int64_t n = (tasks + ROW_NT / 64 - 1) / (ROW_NT / 64);
   return (unsigned)(n < (1 << 22) ? n : 1 << 22);
 }
 
 RowArgs row_args(int32_t eb, const void* X, int64_t ldx, int32_t T, int32_t K, int32_t d, const int32_t* rows, void* Xs,
-                 int64_t lds) {
-  return RowArgs{X, ldx, Xs, lds, rows, T, K, T * K, d, row_pieces(d, eb)};
+                 int64_t lds, int* ub) {
+  *ub = unit_bytes((uint64_t)X | (uint64_t)Xs | (uint64_t)(ldx * eb) | (uint64_t)(lds * eb) | (uint64_t)((int64_t)d * eb), eb);
+  const uint32_t bytes = (uint32_t)d * eb;
+  return RowArgs{(const char*)X, ldx * eb, (char*)Xs, lds * eb, rows, T, K, T * K, bytes, row_pieces(bytes, 64)};
 }
 
-int launch_permute(int32_t eb, const RowArgs& a, hipStream_t st) {
-  const dim3 grid(piece_grid(a.T, a.pieces)), block(ROW_NT);
-  if (eb == 4) permute_kernel<uint32_t><<<grid, block, 0, st>>>(a);
-  else if (eb == 2) permute_kernel<uint16_t><<<grid, block, 0, st>>>(a);
-  else permute_kernel<uint8_t><<<grid, block, 0, st>>>(a);
+int launch_permute(const RowArgs& a, int ub, hipStream_t st) {
+  const dim3 grid(task_grid((int64_t)a.T * a.pieces)), block(ROW_NT);
+  if (ub == 16) permute_kernel<16><<<grid, block, 0, st>>>(a);
+  else if (ub == 4) permute_kernel<4><<<grid, block, 0, st>>>(a);
+  else if (ub == 2) permute_kernel<2><<<grid, block, 0, st>>>(a);
+  else permute_kernel<1><<<grid, block, 0, st>>>(a);
   const int rc = fpi::check_launch("permute_kernel");
   return rc ? rc : fpi::ok();
 }
 
-int launch_dispatch_few(int32_t eb, const SortArgs& s, const RowArgs& a, hipStream_t st) {
+int launch_dispatch_few(const SortArgs& s, const RowArgs& a, int ub, hipStream_t st) {
   const dim3 grid((unsigned)(a.T * a.pieces + 1)), block(ROW_NT);
-  if (eb == 4) dispatch_few_kernel<uint32_t><<<grid, block, 0, st>>>(s, a);
-  else if (eb == 2) dispatch_few_kernel<uint16_t><<<grid, block, 0, st>>>(s, a);
-  else dispatch_few_kernel<uint8_t><<<grid, block, 0, st>>>(s, a);
+  if (ub == 16) dispatch_few_kernel<16><<<grid, block, 0, st>>>(s, a);
+  else if (ub == 4) dispatch_few_kernel<4><<<grid, block, 0, st>>>(s, a);
+  else if (ub == 2) dispatch_few_kernel<2><<<grid, block, 0, st>>>(s, a);
+  else dispatch_few_kernel<1><<<grid, block, 0, st>>>(s, a);
   const int rc = fpi::check_launch("dispatch_few_kernel");
   return rc ? rc : fpi::ok();
+}
+
+template <typename E, int UB>
+void launch_combine_u(const CombineArgs& a, hipStream_t st) {
+  const dim3 grid(task_grid((int64_t)a.T * a.pieces)), block(ROW_NT);
+  if (grid.x <= 1024) combine_kernel<E, UB, 8><<<grid, block, 0, st>>>(a);
+  else combine_kernel<E, UB, 4><<<grid, block, 0, st>>>(a);
+}
+template <typename E>
+void launch_combine(const CombineArgs& a, int ub, hipStream_t st) {
+  if (ub == 16) return launch_combine_u<E, 16>(a, st);
+  if constexpr (sizeof(E) == 2) {
+    if (ub == 2) return launch_combine_u<E, 2>(a, st);
+  }
+  launch_combine_u<E, 4>(a, st);
+}
+
+template <typename E>
+void launch_combine_backward(const CombineBwdArgs& a, int ub, hipStream_t st) {
+  const dim3 grid(row_grid(a.T)), block(ROW_NT);
+  if (ub == 16) return combine_backward_kernel<E, 16><<<grid, block, 0, st>>>(a);
+  if constexpr (sizeof(E) == 2) {
+    if (ub == 2) return combine_backward_kernel<E, 2><<<grid, block, 0, st>>>(a);
+  }
+  combine_backward_kernel<E, 4><<<grid, block, 0, st>>>(a);
 }
 
 int launch_sort(SortArgs a, hipStream_t st) {
@@ -464,6 +500,7 @@ int check_sort(const char* fn, const void* ids, int32_t id_bytes, int32_t T, int
 int check_rows(const char* fn, const void* p, int64_t ld, int32_t d, int eb) {
   if (d < 0) return fpi::fail(FP_EARG, "%s: negative size", fn);
   if (ld < d) return fpi::fail(FP_ESHAPE, "%s: leading dimension too small", fn);
+  if ((int64_t)d * eb > 0x7FFFFFF0) return fpi::fail(FP_ESHAPE, "%s: rows of %lld bytes", fn, (long long)d * eb);
   if ((uintptr_t)p % eb) return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
   return FP_OK;
 }
@@ -502,7 +539,9 @@ extern "C" int fp_moe_permute(int32_t elem_bytes, const void* X, int64_t ldx, in
   const int rc = check_permute("fp_moe_permute", elem_bytes, X, ldx, T, K, d, rows, Xs, lds);
   if (rc) return rc;
   if (T == 0 || d == 0) return fpi::ok();
-  return launch_permute(elem_bytes, row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds), stream);
+  int ub;
+  const RowArgs a = row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds, &ub);
+  return launch_permute(a, ub, stream);
 }
 
 extern "C" int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, int32_t d, const void* ids,
@@ -513,13 +552,19 @@ extern "C" int fp_moe_dispatch(int32_t elem_bytes, const void* X, int64_t ldx, i
   int rc = check_sort(fn, ids, id_bytes, T, K, E, offsets, slots, tokens, rows, ws, ws_bytes);
   if (rc || (rc = check_permute(fn, elem_bytes, X, ldx, T, K, d, rows, Xs, lds))) return rc;
   const SortArgs sa{ids, id_bytes == 8, T * K, K, E, 0, 0, offsets, slots, tokens, rows, (int32_t*)ws};
-  const RowArgs ra = row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds);
-  // few slots in one launch: every workgroup reads all ids for each of its token's choices
-  if (T > 0 && d > 0 && T * K <= SORT_FUSED && K <= 16 && (int64_t)T * ra.pieces <= (1 << 22))
-    return launch_dispatch_few(elem_bytes, sa, ra, stream);
+  int ub;
+  RowArgs ra = row_args(elem_bytes, X, ldx, T, K, d, rows, Xs, lds, &ub);
+  // few slots in one launch: every workgroup reads all ids and ranks its token's choices
+  if (T > 0 && d > 0 && T * K <= SORT_FUSED && K <= 16) {
+    const int32_t pieces = row_pieces(ra.bytes, ROW_NT);
+    if ((int64_t)T * pieces <= (1 << 22)) {
+      ra.pieces = pieces;
+      return launch_dispatch_few(sa, ra, ub, stream);
+    }
+  }
   rc = launch_sort(sa, stream);
   if (rc || T == 0 || d == 0) return rc;
-  return launch_permute(elem_bytes, ra, stream);
+  return launch_permute(ra, ub, stream);
 }
 
 extern "C" int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n_rows, const int32_t* rows,
@@ -534,12 +579,12 @@ extern "C" int fp_moe_combine(fp_dtype dt, const void* O, int64_t ldo, int32_t n
   if ((rc = check_rows(fn, O, ldo, d, eb)) || (rc = check_rows(fn, Y, ldy, d, eb))) return rc;
   if (T == 0 || d == 0) return fpi::ok();
   if ((n_rows > 0 && !O) || !rows || !Y) return fpi::fail(FP_EARG, "%s: null pointer", fn);
-  const CombineArgs a{O, ldo, rows, w, T, K, n_rows, d, row_pieces(d, eb), Y, ldy};
-  const dim3 grid(piece_grid(T, a.pieces)), block(ROW_NT);
-  const bool few = grid.x <= 1024;
-  if (dt == FP_F32) few ? combine_kernel<float, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<float, 4><<<grid, block, 0, stream>>>(a);
-  else if (dt == FP_F16) few ? combine_kernel<__half, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<__half, 4><<<grid, block, 0, stream>>>(a);
-  else few ? combine_kernel<__hip_bfloat16, 8><<<grid, block, 0, stream>>>(a) : combine_kernel<__hip_bfloat16, 4><<<grid, block, 0, stream>>>(a);
+  const int ub = unit_bytes((uint64_t)O | (uint64_t)Y | (uint64_t)(ldo * eb) | (uint64_t)(ldy * eb) | (uint64_t)((int64_t)d * eb), eb);
+  const uint32_t bytes = (uint32_t)d * eb;
+  const CombineArgs a{(const char*)O, ldo * eb, rows, w, T, K, n_rows, row_pieces(bytes, 64), bytes, (char*)Y, ldy * eb};
+  if (dt == FP_F32) launch_combine<float>(a, ub, stream);
+  else if (dt == FP_F16) launch_combine<__half>(a, ub, stream);
+  else launch_combine<__hip_bfloat16>(a, ub, stream);
   rc = fpi::check_launch("combine_kernel");
   return rc ? rc : fpi::ok();
 }
@@ -556,11 +601,13 @@ extern "C" int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy
   if ((rc = check_rows(fn, dY, lddy, d, eb)) || (rc = check_rows(fn, O, ldo, d, eb)) || (rc = check_rows(fn, dO, lddo, d, eb))) return rc;
   if (T == 0) return fpi::ok();
   if (!rows || !w || !dw || (d > 0 && (!dY || (n_rows > 0 && (!O || !dO))))) return fpi::fail(FP_EARG, "%s: null pointer", fn);
-  const CombineBwdArgs a{dY, lddy, O, ldo, rows, w, T, K, n_rows, d, dO, lddo, dw};
-  const dim3 grid(row_grid(T)), block(ROW_NT);
-  if (dt == FP_F32) combine_backward_kernel<float><<<grid, block, 0, stream>>>(a);
-  else if (dt == FP_F16) combine_backward_kernel<__half><<<grid, block, 0, stream>>>(a);
-  else combine_backward_kernel<__hip_bfloat16><<<grid, block, 0, stream>>>(a);
+  const int ub = unit_bytes((uint64_t)dY | (uint64_t)O | (uint64_t)dO | (uint64_t)(lddy * eb) | (uint64_t)(ldo * eb) |
+                                (uint64_t)(lddo * eb) | (uint64_t)((int64_t)d * eb), eb);
+  const CombineBwdArgs a{(const char*)dY, lddy * eb, (const char*)O, ldo * eb, rows, w, T, K, n_rows, (uint32_t)d * eb,
+                         (char*)dO, lddo * eb, dw};
+  if (dt == FP_F32) launch_combine_backward<float>(a, ub, stream);
+  else if (dt == FP_F16) launch_combine_backward<__half>(a, ub, stream);
+  else launch_combine_backward<__hip_bfloat16>(a, ub, stream);
   rc = fpi::check_launch("combine_backward_kernel");
   return rc ? rc : fpi::ok();
 }
