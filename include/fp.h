@@ -295,7 +295,8 @@ size_t fp_scaled_linear_workspace(int32_t T, int32_t d_in);
  * Output row i is made from row rows[i] of X (device int32 [n_rows], e.g.
  * fp_moe_sort's tokens; NULL: row i), X having x_rows rows and x_scale as many
  * entries. Output rows of no group, and rows whose index is outside
- * [0, x_rows), are left as they were. G <= FP_MAX_GROUPS. */
+ * [0, x_rows), are left as they were; with x_rows = 0, X and x_scale may be
+ * NULL. G <= FP_MAX_GROUPS. */
 int fp_scaled_matmul_grouped(const int8_t* X, int64_t ldx, const float* x_scale, int32_t x_rows, const int32_t* rows,
                              int32_t n_rows, const int8_t* const* Wp, const float* w_scale, const float* bias,
                              int64_t ld_scale, const int32_t* offsets, int32_t G, int32_t d_in, int32_t d_out,

@@ -401,3 +401,13 @@ def test_wrong_device(fp):
     with pytest.raises(ValueError, match="device"):
         fp.scaled_matmul(torch.zeros((2, 64), dtype=torch.int8), torch.ones(2), Wp, torch.ones(32, device="cuda"),
                          out=torch.zeros((2, 32), device="cuda"))
+
+
+def test_grouped_without_tokens(fp):
+    """X of no rows: every row's index is outside it, so all are left as they were."""
+    rng = np.random.default_rng(14)
+    _, _, W, ws, bias, off, rows, n = group_inputs(rng, [2, 3], 4, 64, 40)
+    X, xs = torch.empty((0, 64), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    y = torch.full((n, 40), 9.0, device="cuda")
+    fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), ws, off, rows=torch.full_like(rows, -1), bias=bias, out=y)
+    assert bool((y == 9).all())

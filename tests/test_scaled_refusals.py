@@ -176,3 +176,14 @@ def test_binding_moe():
         fp.moe_combine_backward(X.half(), O, plan, w)
     with pytest.raises(ValueError):
         fp.moe_combine_backward(X, O, plan, w, dw=torch.zeros(2, 3))
+
+
+def test_grouped_without_tokens():
+    """X of no rows, as a batch of padding rows alone has it: nothing to do, and no pointers to X and its scales needed."""
+    W = (ctypes.c_void_p * 3)(256, 256, 256)
+
+    def call(X=None, xs=None, x_rows=0, ws=D, Y=D):
+        return fp.lib().fp_scaled_matmul_grouped(X, 64, xs, x_rows, D, 8, W, ws, None, 32, D, 3, 64, 32, BF16, Y, 32, None, 32, None)
+    assert call() == 0
+    assert call(ws=None) == EARG and call(Y=None) == EARG
+    assert call(X=D, x_rows=4) == EARG and call(xs=D, x_rows=4) == EARG

@@ -631,15 +631,17 @@ int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_d
 
 int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
 
-// What the product calls share: sizes, pointers, and how X may be read.
-int check_product(const char* fn, const void* X, int64_t ldx, const float* x_scale, const float* w_scale,
+// What the product calls share: sizes, pointers, and how X may be read. T rows
+// are made from x_rows rows of X (if X has none, it and its scales may be NULL).
+int check_product(const char* fn, const void* X, int64_t ldx, int32_t x_rows, const float* x_scale, const float* w_scale,
                   const float* bias, int32_t T, int32_t d_in, int32_t d_out, fp_dtype y_dt, const void* Y, int64_t ldy,
                   const int32_t* Z, int64_t ldz) {
   if (T < 0 || d_in < 0 || d_out < 0) return fpi::fail(FP_EARG, "%s: negative size", fn);
   if (!elem_bytes(y_dt)) return fpi::fail(FP_EARG, "%s: unknown output type %d", fn, (int)y_dt);
   if (d_in > FP_MAX_DIN) return fpi::fail(FP_ESHAPE, "%s: d_in=%d > %d", fn, d_in, FP_MAX_DIN);
   if (ldx < d_in || ldy < d_out || (Z && ldz < d_out)) return fpi::fail(FP_ESHAPE, "%s: leading dimension too small", fn);
-  if (T > 0 && d_out > 0 && ((d_in > 0 && !X) || !x_scale || !w_scale || !Y)) return fpi::fail(FP_EARG, "%s: null pointer", fn);
+  if (T > 0 && d_out > 0 && ((x_rows > 0 && ((d_in > 0 && !X) || !x_scale)) || !w_scale || !Y))
+    return fpi::fail(FP_EARG, "%s: null pointer", fn);
   if (((uintptr_t)Y) % elem_bytes(y_dt) || ((uintptr_t)Z) % 4 || ((uintptr_t)x_scale) % 4 || ((uintptr_t)w_scale) % 4 ||
       ((uintptr_t)bias) % 4)
     return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
@@ -700,7 +702,7 @@ extern "C" int fp_scaled_matmul(const int8_t* X, int64_t ldx, const float* x_sca
                                 const float* w_scale, const float* bias, int32_t T, int32_t d_in, int32_t d_out,
                                 fp_dtype y_dt, void* Y, int64_t ldy, int32_t* Z, int64_t ldz, hipStream_t stream) {
   const char* fn = "fp_scaled_matmul";
-  const int rc = check_product(fn, X, ldx, x_scale, w_scale, bias, T, d_in, d_out, y_dt, Y, ldy, Z, ldz);
+  const int rc = check_product(fn, X, ldx, T, x_scale, w_scale, bias, T, d_in, d_out, y_dt, Y, ldy, Z, ldz);
   if (rc) return rc;
   if (T == 0 || d_out == 0) return fpi::ok();
   if (d_in > 0 && !Wp) return fpi::fail(FP_EARG, "%s: null pointer", fn);
@@ -730,7 +732,7 @@ extern "C" int fp_scaled_linear(fp_dtype x_dt, const void* X, int64_t ldx, const
   float* scale = (float*)ws;
   int8_t* Xq = (int8_t*)ws + fpi::align_up((size_t)T * 4, 256);
   const int64_t ldq = chunked(d_in);
-  rc = check_product(fn, Xq, ldq, scale, w_scale, bias, T, d_in, d_out, y_dt, Y, ldy, Z, ldz);
+  rc = check_product(fn, Xq, ldq, T, scale, w_scale, bias, T, d_in, d_out, y_dt, Y, ldy, Z, ldz);
   if (rc) return rc;
   if (T == 0 || d_out == 0) return fpi::ok();
   if (d_in > 0 && !Wp) return fpi::fail(FP_EARG, "%s: null pointer", fn);
@@ -749,7 +751,7 @@ extern "C" int fp_scaled_matmul_grouped(const int8_t* X, int64_t ldx, const floa
                                         const int32_t* offsets, int32_t G, int32_t d_in, int32_t d_out, fp_dtype y_dt,
                                         void* Y, int64_t ldy, int32_t* Z, int64_t ldz, hipStream_t stream) {
   const char* fn = "fp_scaled_matmul_grouped";
-  const int rc = check_product(fn, X, ldx, x_scale, w_scale, bias, n_rows, d_in, d_out, y_dt, Y, ldy, Z, ldz);
+  const int rc = check_product(fn, X, ldx, x_rows, x_scale, w_scale, bias, n_rows, d_in, d_out, y_dt, Y, ldy, Z, ldz);
   if (rc) return rc;
   if (G < 1 || G > FP_MAX_GROUPS) return fpi::fail(FP_EARG, "%s: G=%d outside [1, %d]", fn, G, FP_MAX_GROUPS);
   if (x_rows < 0 || (!rows && x_rows < n_rows)) return fpi::fail(FP_ESHAPE, "%s: x_rows=%d for %d rows", fn, x_rows, n_rows);
