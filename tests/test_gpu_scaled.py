@@ -411,3 +411,14 @@ def test_grouped_without_tokens(fp):
     y = torch.full((n, 40), 9.0, device="cuda")
     fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), ws, off, rows=torch.full_like(rows, -1), bias=bias, out=y)
     assert bool((y == 9).all())
+
+
+def test_one_group_with_rows_of_scales_apart(fp):
+    """One group's scales and bias may be rows of matrices of any width."""
+    rng = np.random.default_rng(15)
+    X, xs, W, ws, bias, off, rows, n = group_inputs(rng, [7], 5, 64, 40)
+    wide = torch.zeros((3, 50), device="cuda")
+    wide[1, :40] = bias[0]
+    _, Y, mag = reference(X[rows.long()], W[0], xs[rows.long()], ws[0], bias[0])
+    for b, w in ((wide[1:2, :40], ws), (bias, torch.cat([ws, ws], 1)[:, :40])):
+        close(fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), w, off, rows=rows, bias=b, dtype=torch.float32), Y, mag, torch.float32)
