@@ -262,7 +262,10 @@ int fp_witness_linear_packed_with_sumcheck(const int8_t* X, int64_t ldx, const i
  * once to Y's type (FP_F32, FP_F16 or FP_BF16). X: int8 [T, d_in] (leading dim
  * ldx, any alignment; rows that start on 16 bytes with ldx a multiple of 16
  * and at least ceil(d_in / 16) * 16 are read in whole 16-byte chunks, those of
- * the last row included, and the bytes past d_in do not count). Wp: the
+ * the last row included, and the bytes past d_in do not count: storage that
+ * ends inside the last row's chunk is for the caller to copy into padded rows,
+ * as the Python binding does, or its row to be given alone with ldx = d_in,
+ * which reads d_in bytes). Wp: the
  * weights from fp_witness_pack_weights. x_scale [T], w_scale [d_out], bias
  * [d_out] or NULL: device fp32. Y [T, d_out] (ldy >= d_out); Z int32 (ldz) or
  * NULL: not stored. d_in <= FP_MAX_DIN. */

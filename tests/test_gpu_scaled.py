@@ -422,3 +422,25 @@ def test_one_group_with_rows_of_scales_apart(fp):
     _, Y, mag = reference(X[rows.long()], W[0], xs[rows.long()], ws[0], bias[0])
     for b, w in ((wide[1:2, :40], ws), (bias, torch.cat([ws, ws], 1)[:, :40])):
         close(fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), w, off, rows=rows, bias=b, dtype=torch.float32), Y, mag, torch.float32)
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(2, 100, 70), (9, 20, 96), (40, 1000, 60), (300, 333, 515), (700, 65, 1300)])
+def test_rows_that_end_with_their_storage(fp, T, d_in, d_out):
+    """Rows 16 bytes apart whose last one ends with the storage, in the middle of a 16-byte chunk."""
+    rng = np.random.default_rng(T)
+    ld = (d_in + 15) // 16 * 16
+    _, W, xs, ws, bias = inputs(rng, T, d_in, d_out)
+    buf = torch.from_numpy(rng.integers(-128, 128, size=(T - 1) * ld + d_in, dtype=np.int8)).cuda()
+    X = torch.as_strided(buf, (T, d_in), (ld, 1))
+    assert X.data_ptr() % 16 == 0 and buf.untyped_storage().nbytes() < T * ld
+    Z, Y, mag = reference(X, W, xs, ws, bias)
+    z = torch.zeros((T, d_out), dtype=torch.int32, device="cuda")
+    Wp = fp.pack_weights(W)
+    close(fp.scaled_matmul(X, xs, Wp, ws, bias=bias, dtype=torch.float32, Z=z), Y, mag, torch.float32)
+    assert np.array_equal(z.cpu().numpy(), Z.astype(np.int64))
+    off = torch.tensor([0, T // 3, T], dtype=torch.int32, device="cuda")
+    back = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    y = fp.scaled_matmul_grouped(X, xs, fp.PackedExperts([Wp, Wp]), torch.stack([ws, ws]), off, rows=back,
+                                 bias=torch.stack([bias, bias]), dtype=torch.float32, Z=z)
+    close(y, Y[::-1], mag[::-1], torch.float32)
+    assert np.array_equal(z.cpu().numpy(), Z[::-1].astype(np.int64))

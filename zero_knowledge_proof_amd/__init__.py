@@ -671,6 +671,18 @@ def _whole_rows(X, ld: int) -> int:
     return ld
 
 
+def _readable(X, ld: int):
+    """X and the leading dimension that a product reads it with: where the last row's chunk is not in X's storage, a copy
+    with padded rows."""
+    try:
+        return X, _whole_rows(X, ld)
+    except ValueError:
+        T, d = X.shape
+        up = (d + 15) // 16 * 16
+        copy = torch.empty((T, up), dtype=X.dtype, device=X.device)[:, :d]
+        return copy.copy_(X), up
+
+
 def quantize_rows(X, out=None, scale=None):
     """(Xq, scale): each row of X [T, d] (float32, float16 or bfloat16) as int8 with the scale max|x| / 127, rounded to
     the nearest (ties to even). Without ``out``, Xq's rows are a multiple of 16 bytes apart, so that the products read
@@ -718,7 +730,7 @@ def scaled_matmul(X, x_scale, Wp: PackedWeights, w_scale, bias=None, out=None, d
     if bias is not None:
         _vector(bias, torch.float32, (d_out,), "bias")
     out, dt, ldy, z, ldz = _product_out(T, d_out, out, dtype, Z, X.device)
-    ldx = _whole_rows(X, ldx)
+    X, ldx = _readable(X, ldx)
     st = _here(X, x_scale, Wp.data, w_scale, bias, out, Z)
     _check(lib().fp_scaled_matmul(X.data_ptr(), ldx, x_scale.data_ptr(), Wp.data.data_ptr(), w_scale.data_ptr(),
                                   0 if bias is None else bias.data_ptr(), T, d_in, d_out, dt, out.data_ptr(), ldy, z,
@@ -789,7 +801,7 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
         n = rows.numel()
         _vector(rows, torch.int32, (n,), "rows")
     out, dt, ldy, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
-    ldx = _whole_rows(X, ldx)
+    X, ldx = _readable(X, ldx)
     st = _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
     _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), ldx, x_scale.data_ptr(), x_rows,
                                           0 if rows is None else rows.data_ptr(), n, We.ptrs, w_scale.data_ptr(),
