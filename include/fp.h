@@ -299,7 +299,10 @@ size_t fp_scaled_linear_workspace(int32_t T, int32_t d_in);
  * fp_moe_sort's tokens; NULL: row i), X having x_rows rows and x_scale as many
  * entries. Output rows of no group, and rows whose index is outside
  * [0, x_rows), are left as they were; with x_rows = 0, X and x_scale may be
- * NULL. G <= FP_MAX_GROUPS. */
+ * NULL. G <= FP_MAX_GROUPS: the launch's arguments hold the groups' pointers.
+ * Of more experts (fp_moe_sort takes FP_MAX_EXPERTS), those from g on are a call
+ * with offsets + g, Wp + g, w_scale + g ld_scale and bias likewise into the same
+ * Y and Z, as the Python binding makes for every FP_MAX_GROUPS of them. */
 int fp_scaled_matmul_grouped(const int8_t* X, int64_t ldx, const float* x_scale, int32_t x_rows, const int32_t* rows,
                              int32_t n_rows, const int8_t* const* Wp, const float* w_scale, const float* bias,
                              int64_t ld_scale, const int32_t* offsets, int32_t G, int32_t d_in, int32_t d_out,

@@ -444,3 +444,27 @@ def test_rows_that_end_with_their_storage(fp, T, d_in, d_out):
                                  bias=torch.stack([bias, bias]), dtype=torch.float32, Z=z)
     close(y, Y[::-1], mag[::-1], torch.float32)
     assert np.array_equal(z.cpu().numpy(), Z[::-1].astype(np.int64))
+
+
+@pytest.mark.parametrize("G,most,d_in", [(257, 3, 64), (300, 9, 100), (1024, 2, 33), (512, 0, 64)])
+def test_grouped_of_many_experts(fp, G, most, d_in):
+    """More groups than one launch takes; rows behind the last group are left as they were."""
+    rng = np.random.default_rng(G)
+    counts = rng.integers(0, most + 1, G)
+    X, xs, W, ws, bias, off, rows, n = group_inputs(rng, counts, 20, d_in, 40, True, 3)
+    rows[n // 2] = -1
+    y = torch.full((n, 40), 9.0, device="cuda")
+    z = torch.full((n, 40), 9, dtype=torch.int32, device="cuda")
+    fp.scaled_matmul_grouped(X, xs, fp.pack_experts(W), ws, off, rows=rows, bias=bias, out=y, Z=z)
+    o, r = off.tolist(), rows.tolist()
+    left = np.ones(n, bool)
+    for g in range(G):
+        for i in range(o[g], o[g + 1]):
+            if r[i] < 0:
+                continue
+            left[i] = False
+            Z, Y, mag = reference(X[r[i]:r[i] + 1], W[g], xs[r[i]:r[i] + 1], ws[g], bias[g])
+            assert np.array_equal(z[i:i + 1].cpu().numpy(), Z.astype(np.int64))
+            close(y[i:i + 1], Y, mag, torch.float32)
+    left = torch.from_numpy(left).cuda()
+    assert int(left.sum()) >= 3 and bool((y[left] == 9).all()) and bool((z[left] == 9).all())

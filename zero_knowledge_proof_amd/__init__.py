@@ -16,6 +16,7 @@ import torch
 
 P = 0xFFFFFFFF00000001
 FP_I8, FP_I32, FP_F32, FP_F16, FP_BF16 = 0, 1, 2, 3, 4
+MAX_GROUPS = 256  # FP_MAX_GROUPS
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfp.so")
 EXPORTS = [
@@ -773,6 +774,9 @@ class PackedExperts:
         if any(w.data.device != self.device for w in weights):
             raise ValueError("experts on different devices")
         self.ptrs = (ctypes.c_void_p * len(weights))(*[w.data.data_ptr() for w in weights])
+        # (first expert, how many, their addresses in ptrs): a launch takes MAX_GROUPS
+        counts = [(g, min(MAX_GROUPS, len(weights) - g)) for g in range(0, len(weights), MAX_GROUPS)]
+        self.parts = [(g, n, (ctypes.c_void_p * n).from_buffer(self.ptrs, g * ctypes.sizeof(ctypes.c_void_p))) for g, n in counts]
 
     def __len__(self):
         return len(self.weights)
@@ -788,7 +792,8 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
     """scaled_matmul of each expert with its own rows: output rows [offsets[g], offsets[g + 1]) (int32 [G + 1] on the
     device, as moe_sort writes them) by expert g with w_scale[g] (float32 [G, d_out]; bias likewise). Output row i is
     made from X's row rows[i] (int32 on the device, e.g. moe_sort's tokens; None: row i). Rows of no expert are left as
-    they were in ``out`` and Z (a new ``out`` holds whatever its memory held there)."""
+    they were in ``out`` and Z (a new ``out`` holds whatever its memory held there). More than 256 experts take a launch
+    for every 256."""
     G, d_in, d_out = len(We.weights), We.d_in, We.d_out
     ldx = _matrix(X, torch.int8, None, d_in, "X")
     n = x_rows = X.shape[0]
@@ -803,10 +808,13 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
     out, dt, ldy, z, ldz = _product_out(n, d_out, out, dtype, Z, X.device)
     X, ldx = _readable(X, ldx)
     st = _here(X, x_scale, We.weights[0].data, w_scale, offsets, rows, bias, out, Z)
-    _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), ldx, x_scale.data_ptr(), x_rows,
-                                          0 if rows is None else rows.data_ptr(), n, We.ptrs, w_scale.data_ptr(),
-                                          0 if bias is None else bias.data_ptr(), ldw, offsets.data_ptr(), G, d_in,
-                                          d_out, dt, out.data_ptr(), ldy, z, ldz, st), "fp_scaled_matmul_grouped")
+    for g, count, ptrs in We.parts:
+        _check(lib().fp_scaled_matmul_grouped(X.data_ptr(), ldx, x_scale.data_ptr(), x_rows,
+                                              0 if rows is None else rows.data_ptr(), n, ptrs,
+                                              w_scale.data_ptr() + 4 * g * ldw,
+                                              0 if bias is None else bias.data_ptr() + 4 * g * ldw, ldw,
+                                              offsets.data_ptr() + 4 * g, count, d_in, d_out, dt, out.data_ptr(), ldy, z,
+                                              ldz, st), "fp_scaled_matmul_grouped")
     return out
 
 
