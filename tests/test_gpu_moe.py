@@ -310,3 +310,51 @@ def test_other_stream(fp):
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(y, fp.moe_combine(want, plan))
+
+
+def test_as_functions_of_autograd(fp):
+    """The calls and their gradients as torch's Functions, as a program that trains through them has them: the same
+    gradients as the calls by themselves; outside a Function, a tensor that asks for a gradient is refused."""
+    T, K, E, d = 50, 3, 7, 72
+    rng = np.random.default_rng(4)
+    ids = torch.from_numpy(draw_ids(rng, T, K, E, "wild")).cuda()
+
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, plan):
+            ctx.plan = plan
+            return fp.moe_permute(X, plan, out=X.new_zeros((T * K, d)))
+
+        @staticmethod
+        def backward(ctx, dXs):
+            return fp.moe_dispatch_backward(dXs.contiguous(), ctx.plan), None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, O, w, plan):  # noqa: E741
+            ctx.save_for_backward(O, w)
+            ctx.plan = plan
+            return fp.moe_combine(O, plan, w)
+
+        @staticmethod
+        def backward(ctx, dY):
+            O, w = ctx.saved_tensors  # noqa: E741
+            return (*fp.moe_combine_backward(dY.contiguous(), O, ctx.plan, w, dO=torch.zeros_like(O)), None)
+
+    plan = fp.moe_sort(ids, E)
+    X = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda()
+    w = torch.from_numpy(rng.random((T, K)).astype(np.float32)).cuda()
+    G = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda()
+    Xs = fp.moe_permute(X, plan, out=torch.zeros((T * K, d), device="cuda"))
+    dO, dw = fp.moe_combine_backward(G, Xs * 3, plan, w, dO=torch.zeros_like(Xs))
+    dX = fp.moe_dispatch_backward(dO * 3, plan)
+    x, v = X.clone().requires_grad_(), w.clone().requires_grad_()
+    y = Combine.apply(Gather.apply(x, plan) * 3, v, plan)
+    gx, gv = torch.autograd.grad(y, (x, v), G)
+    assert torch.equal(y, fp.moe_combine(Xs * 3, plan, w)) and torch.equal(gx, dX) and torch.equal(gv, dw)
+    for f in (lambda: fp.moe_permute(x, plan), lambda: fp.moe_dispatch(x, ids, E), lambda: fp.moe_combine(Xs, plan, v)):
+        with pytest.raises(ValueError, match="backward"):
+            f()
+    with torch.no_grad():
+        assert torch.equal(fp.moe_combine(Xs, plan, v), fp.moe_combine(Xs, plan, w))
+        assert torch.equal(fp.moe_dispatch(x, ids, E)[0][:int(plan.offsets[-1])], Xs[:int(plan.offsets[-1])])

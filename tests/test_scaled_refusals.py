@@ -187,3 +187,19 @@ def test_grouped_without_tokens():
     assert call() == 0
     assert call(ws=None) == EARG and call(Y=None) == EARG
     assert call(X=D, x_rows=4) == EARG and call(xs=D, x_rows=4) == EARG
+
+
+def test_gradients_are_not_lost_silently():
+    """The calls record no graph, so those that have gradients refuse tensors that ask for one."""
+    plan = fp.MoePlan(3, 2, 4, device="cpu")
+    ids = torch.zeros(3, 2, dtype=torch.int32)
+    X, O, w = torch.zeros(3, 8), torch.zeros(6, 8), torch.zeros(3, 2)  # noqa: E741
+    g = lambda t: t.clone().requires_grad_()  # noqa: E731
+    for f in (lambda: fp.moe_permute(g(X), plan), lambda: fp.moe_dispatch(g(X), ids, 4, plan=plan),
+              lambda: fp.moe_combine(g(O), plan, w), lambda: fp.moe_combine(O, plan, g(w)), lambda: fp.moe_combine(g(O), plan),
+              lambda: fp.moe_combine(O, plan, torch.softmax(g(w), 1))):
+        with pytest.raises(ValueError, match="backward"):
+            f()
+        with torch.no_grad(), pytest.raises(Exception) as e:  # on to the next check: these are no device tensors
+            f()
+        assert "backward" not in str(e.value)

@@ -722,7 +722,8 @@ def _product_out(T, d_out, out, dtype, Z, device):
 
 def scaled_matmul(X, x_scale, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=torch.bfloat16, Z=None):
     """Y[t, o] = x_scale[t] w_scale[o] sum_k X[t, k] W[o, k] + bias[o] for int8 X [T, d_in] and packed weights, in
-    ``out``'s type or ``dtype``; Z (int32 [T, d_out] or None) also receives the integer product, the layer's witness."""
+    ``out``'s type or ``dtype``; Z (int32 [T, d_out] or None) also receives the integer product, the layer's witness. The
+    products have no gradients: what they return carries none, whatever the scales and the bias ask for."""
     d_in, d_out = Wp.d_in, Wp.d_out
     ldx = _matrix(X, torch.int8, None, d_in, "X")
     T = X.shape[0]
@@ -819,6 +820,15 @@ def scaled_matmul_grouped(X, x_scale, We: PackedExperts, w_scale, offsets, rows=
 
 
 # ------------------------------------------------------- tokens by expert --
+def _no_graph(name: str, *tensors):
+    """No call here records a graph for autograd: one whose gradient is a call of its own refuses a tensor that asks for
+    a gradient, which would be lost. (Inside a torch.autograd.Function, and under torch.no_grad, nothing asks.)"""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a tensor requires a gradient, which this call does not record: wrap it and %s in a "
+                             "torch.autograd.Function, or detach the tensor" % name)
+
+
 class MoePlan:
     """The device sort of T tokens with K experts each out of E: offsets int32 [E + 1], slots and tokens int32 [T K]
     (sorted row -> slot t K + k, and -> t; -1 past the last row with an expert) and rows int32 [T, K] (slot -> sorted
@@ -880,7 +890,9 @@ def _permute_out(X, plan, out):
 
 def moe_permute(X, plan: MoePlan, out=None):
     """Xs [T K, d]: the tokens' rows X [T, d] in the plan's order. Rows past the last one with an expert are left as
-    they were in ``out`` (a new one holds whatever its memory held there)."""
+    they were in ``out`` (a new one holds whatever its memory held there). Its gradient is moe_dispatch_backward; no graph
+    is recorded, and an X that requires a gradient is refused unless under torch.no_grad."""
+    _no_graph("moe_dispatch_backward", X)
     eb, ldx, out, ldo = _permute_out(X, plan, out)
     st = _here(X, plan.buf, out)
     _check(lib().fp_moe_permute(eb, X.data_ptr(), ldx, plan.T, plan.K, X.shape[1], plan.ptrs[3], out.data_ptr(), ldo,
@@ -889,7 +901,8 @@ def moe_permute(X, plan: MoePlan, out=None):
 
 
 def moe_dispatch(X, ids, n_experts: int, plan: MoePlan | None = None, out=None):
-    """(Xs, plan): moe_sort of ids and moe_permute of X in one call."""
+    """(Xs, plan): moe_sort of ids and moe_permute of X in one call (its gradient: moe_dispatch_backward, as there)."""
+    _no_graph("moe_dispatch_backward", X)
     plan = _sort_args(ids, n_experts, plan)
     eb, ldx, out, ldo = _permute_out(X, plan, out)
     st = _here(X, ids, plan.buf, out)
@@ -919,7 +932,9 @@ def _combine(O, plan, weights, out, name):
 
 def moe_combine(O, plan: MoePlan, weights=None, out=None):
     """Y [T, d]: each token's rows of O [T K, d] (the experts' outputs in the plan's order) added with its weights
-    (float32 [T, K]; None: all one), in fp32, k ascending."""
+    (float32 [T, K]; None: all one), in fp32, k ascending. Its gradients are moe_combine_backward (without weights:
+    moe_permute); no graph is recorded, and tensors that require a gradient are refused unless under torch.no_grad."""
+    _no_graph("moe_combine_backward", O, weights)
     return _combine(O, plan, weights, out, "O")
 
 
