@@ -203,3 +203,14 @@ def test_gradients_are_not_lost_silently():
         with torch.no_grad(), pytest.raises(Exception) as e:  # on to the next check: these are no device tensors
             f()
         assert "backward" not in str(e.value)
+
+
+@pytest.mark.parametrize("T", [1, 9, 300, 2 ** 31 - 1])
+@pytest.mark.parametrize("d_out", [2 ** 31 - 1, 2 ** 31 - 33, 2 ** 31 - 200])
+@pytest.mark.parametrize("ldx", [64, 65])
+def test_sizes_next_to_32_bits(T, d_out, ldx):
+    """Outputs whose number leaves 32 bits when it is rounded up to tiles."""
+    assert mm(T=T, d_out=d_out, ldx=ldx, ldy=d_out, ldz=d_out) == ESHAPE
+    W = (ctypes.c_void_p * 3)(256, 256, 256)
+    assert fp.lib().fp_scaled_matmul_grouped(D, ldx, D, T, D, T, W, D, None, d_out, D, 3, 64, d_out, BF16, D, d_out, None, d_out,
+                                             None) == ESHAPE

@@ -371,9 +371,12 @@ int64_t turns_whole(int64_t tiles) {
   return rest <= 128 ? tiles - rest : tiles;
 }
 
+// n / d rounded up, for n up to 2^31 - 1.
+int64_t parts(int64_t n, int d) { return (n + d - 1) / d; }
+
 template <bool GROUPED>
 int launch_turns(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
-  a.tiles_o = (a.N + 255) / 256;
+  a.tiles_o = (int32_t)parts(a.N, 256);
   a.group_o = 4;
   const int64_t m = GROUPED ? (a.G < a.T ? a.G : a.T) : 1;
   a.tiles_t = (int32_t)((a.T + m * 255) / 256);
@@ -574,7 +577,7 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
 template <int NW, int TM, int XR, int PF, bool GROUPED, bool XV>
 int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
   constexpr int BT = 8 * XR, NT = NW * 64;
-  a.tiles_o = (a.wp_rb + TM - 1) / TM;
+  a.tiles_o = (int32_t)parts(a.wp_rb, TM);
   const int64_t m = GROUPED ? (a.G < a.T ? a.G : a.T) : 1;
   a.tiles_t = (int32_t)((a.T + m * (BT - 1)) / BT);
   const int64_t blocks = (int64_t)a.tiles_t * a.tiles_o;
@@ -616,8 +619,8 @@ int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_d
   } else {
     if (a.T <= 8) return launch_rows<8, 1, 1, 2, false, XV>(fn, a, gp, y_dt, st);
     if constexpr (XV) {
-      const int64_t t32 = (a.T + 31) / 32, t64 = (a.T + 63) / 64, o64 = (a.N + 63) / 64;
-      const int64_t tiles = (int64_t)((a.N + 255) / 256) * ((a.T + 255) / 256), whole = turns_whole(tiles);
+      const int64_t t32 = parts(a.T, 32), t64 = parts(a.T, 64), o64 = parts(a.N, 64);
+      const int64_t tiles = parts(a.N, 256) * parts(a.T, 256), whole = turns_whole(tiles);
       const double turns = 4 + a.wp_kb * (0.86 * (double)((whole + 255) / 256) + (tiles > whole ? 0.5 : 0.0));
       const double rows = 3 + a.wp_kb * 0.115 * (double)((o64 * t64 + 255) / 256);
       constexpr int64_t FILL = 192;  // workgroups that occupy most of the CUs
@@ -653,8 +656,8 @@ void fill_args(ScaledArgs& a, const int8_t* X, int64_t ldx, const float* x_scale
                int32_t* Z, int64_t ldz) {
   a.X = X; a.ldx = ldx; a.xs = x_scale; a.ws = w_scale; a.bias = bias;
   a.T = T; a.K = d_in; a.N = d_out; a.Y = Y; a.ldy = ldy; a.Z = Z; a.ldz = ldz;
-  a.wp_rb = (d_out + 31) / 32;
-  a.wp_kb = (d_in + WP_BK - 1) / WP_BK;
+  a.wp_rb = (int32_t)parts(d_out, 32);
+  a.wp_kb = (int32_t)parts(d_in, WP_BK);
   a.vecY = (((uintptr_t)Y) & 15) == 0 && (ldy * elem_bytes(y_dt)) % 16 == 0;
   a.vecZ = (((uintptr_t)Z) & 15) == 0 && ldz % 4 == 0;
 }
