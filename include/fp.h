@@ -268,7 +268,8 @@ int fp_witness_linear_packed_with_sumcheck(const int8_t* X, int64_t ldx, const i
  * which reads d_in bytes). Wp: the
  * weights from fp_witness_pack_weights. x_scale [T], w_scale [d_out], bias
  * [d_out] or NULL: device fp32. Y [T, d_out] (ldy >= d_out); Z int32 (ldz) or
- * NULL: not stored. d_in <= FP_MAX_DIN. */
+ * NULL: not stored. d_in <= FP_MAX_DIN; a product of more tiles than one launch
+ * of 2^31 - 1 threads makes is refused (FP_ESHAPE), here and below. */
 int fp_scaled_matmul(const int8_t* X, int64_t ldx, const float* x_scale, const int8_t* Wp, const float* w_scale,
                      const float* bias, int32_t T, int32_t d_in, int32_t d_out, fp_dtype y_dt, void* Y, int64_t ldy,
                      int32_t* Z, int64_t ldz, hipStream_t stream);
@@ -277,8 +278,9 @@ int fp_scaled_matmul(const int8_t* X, int64_t ldx, const float* x_scale, const i
  * Xq[t, k] = rint(X[t, k] * (127 * (1 / a))) (each step in fp32, ties to even;
  * |Xq| <= 127). X:
  * FP_F32, FP_F16 or FP_BF16 [T, cols] (ldx); Xq int8 (ldq >= cols). A row of
- * zeros has scale 0; a row with an infinity or a NaN has scale NaN and zeros,
- * so that a product with it is NaN. */
+ * zeros has scale 0, and one whose a / 127 is below fp32's normal numbers a scale
+ * with the few bits it has there (0 at the least); a row with an infinity or a
+ * NaN has scale NaN and zeros, so that a product with it is NaN. */
 int fp_quantize_rows(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t cols, int8_t* Xq, int64_t ldq,
                      float* scale, hipStream_t stream);
 

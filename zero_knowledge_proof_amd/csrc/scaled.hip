@@ -24,10 +24,13 @@ using sdev::v4f;
 
 // ---- row quantization ------------------------------------------------------
 // scale = max |x| / 127, q = rint(x * (127 * (1 / max |x|))), each step rounded
-// to fp32: |x - q scale| <= (1/2 + 2^-15) scale. Below 2^-100 the
-// reciprocal would leave fp32, so such a row is first multiplied by 2^64
-// (exact); a row of zeros gets scale 0 and zeros; a row with an infinity or a
-// NaN gets scale NaN and zeros, so that every product with it is NaN.
+// to fp32: |x - q scale| <= (1/2 + 2^-15) scale (four roundings of at most 127
+// steps) for a maximum from 127 * 2^-126 to 2^126. Above, 1 / max |x| is
+// subnormal and the bound 1/2 + 2^-14; below, the scale is, with as few bits as
+// it has there (2^-149 / 127 rounds to 0). Below 2^-100 the reciprocal would
+// leave fp32, so such a row is first multiplied by 2^64 (exact); a row of zeros
+// gets scale 0 and zeros; a row with an infinity or a NaN gets scale NaN and
+// zeros, so that every product with it is NaN.
 struct QuantArgs {
   const void* X;
   int64_t ldx;
@@ -145,8 +148,10 @@ struct ScaleTables {
 // in L1. X is staged two blocks (whole 128-byte lines) at a time.
 // Measured: 8192 x 8192 -> 8192 in 441-463 us (2.4-2.5 POP/s), the matrix cores
 // busy 67% of the cycles at a clock that the power limit holds at 1.68 GHz; 4096
-// x 4096 -> 14336 in 226-235 us; 512 tokens of it in 36 us, latency-bound (2.44
-// GHz, busy 24%). Without the alternation (one barrier a stage) 3-7% slower,
+// x 4096 -> 14336 in 226-235 us; 512 tokens of it in 37 us, with Z 43-45 us,
+// latency-bound (2.45 GHz, busy 26%): the three bodies share a kernel, so the
+// narrow ones have the widest's 256 registers and 76 KiB and a CU holds one
+// workgroup, whose prologue and stores nothing overlaps. Without the alternation (one barrier a stage) 3-7% slower,
 // with raised priority around the products 10%; weights two or four blocks ahead
 // 2% slower. Waves of 32 outputs x all tokens, which load no weight fragment
 // twice but read twice as much X from LDS: 2% slower for 256 tokens, the same or
@@ -405,7 +410,7 @@ int launch_turns(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_d
 // from memory touch 32 rows a load: 38 us against 19 us for 64 tokens, K =
 // 14336, 4096 outputs.) The waves' sums meet in LDS (integers: any order gives
 // the same), 32 tokens at a time, and a thread finishes four outputs of a row in
-// the 64-output tiles (one each: 777 tokens of 1008 -> 1003 7.0 us, four 6.0),
+// the 64-output tiles (one each: 777 tokens of 1008 -> 1003, bf16 7.0 us, four 6.1),
 // one in the 32-output ones (one token, 4096 -> 14336: 10.4 us, four 10.9).
 template <int NW, int TM, int XR, int PF, bool GROUPED, bool XV, typename YT>
 __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, GroupPtrs gp) {
@@ -605,10 +610,16 @@ int launch_rows(const char* fn, ScaledArgs a, const GroupPtrs& gp, fp_dtype y_dt
 // Groups: by the rows a group has on average, more than two take the turns
 // kernel (2048 rows in 128 groups, 5120 -> 8192: 0.90 ms, 64 x 64 1.04, 32 x 32
 // 1.29; 400 rows in 60 groups, 1024 -> 1024: 15.1 us, 18.8, 25.3), fewer the
-// 8-row tiles (16 rows in 16 groups, 4096 -> 14336: 114 us; turns 133).
+// 8-row tiles (16 rows in 16 groups, 4096 -> 14336: 114 us; turns 133). Both
+// sides of the rule were measured at 16 groups and 1024 outputs and above only.
+// Its average knows neither the number of outputs nor skew, and no tile splits
+// K over workgroups: few tiles of a deep K leave most CUs idle (32 rows in 8
+// groups, 8192 -> 1024: 52 us, its weights' bytes 11; one token, 16384 -> 1024:
+// 8.3, its weights' 2.8).
 // Rows of X that are not whole 16-byte chunks are read at whatever address they
 // have (the last bytes one by one) in 8-row or 64 x 64 tiles (777 rows of 1000
-// bytes, 1003 outputs: 18.6 us, padded 6.7; a byte at a time 33.7).
+// bytes, 1003 outputs, bf16: 18.4 us, padded 6.1; a byte at a time 33.7; 4096
+// rows of 4097 bytes, 14336 outputs: 872 us, padded 250).
 template <bool GROUPED, bool XV>
 int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_dtype y_dt, hipStream_t st) {
   if constexpr (GROUPED) {
