@@ -358,3 +358,42 @@ def test_as_functions_of_autograd(fp):
     with torch.no_grad():
         assert torch.equal(fp.moe_combine(Xs, plan, v), fp.moe_combine(Xs, plan, w))
         assert torch.equal(fp.moe_dispatch(x, ids, E)[0][:int(plan.offsets[-1])], Xs[:int(plan.offsets[-1])])
+
+
+def test_gradients_replayed(fp):
+    """There and back and both gradients captured with a kept plan, replayed on other choices and values, with the same
+    calls on another stream and another plan between the replays: each replay against the calls by themselves."""
+    T, K, E, d = 70, 3, 9, 75
+    rng = np.random.default_rng(6)
+
+    def step(plan, X, ids, w, G):
+        Xs, _ = fp.moe_dispatch(X, ids, E, plan=plan, out=torch.zeros((T * K, d), dtype=X.dtype, device="cuda"))
+        Y = fp.moe_combine(Xs, plan, w)
+        dO, dw = fp.moe_combine_backward(G, Xs, plan, w, dO=torch.zeros_like(Xs))
+        return Xs, Y, dO, dw, fp.moe_dispatch_backward(dO, plan), *fp.quantize_rows(Y)
+
+    def values(kind):
+        X, G = (torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda().bfloat16() for _ in range(2))
+        return (X, torch.from_numpy(draw_ids(rng, T, K, E, kind)).cuda(),
+                torch.from_numpy(rng.random((T, K)).astype(np.float32)).cuda(), G)
+    sets = [values(kind) for kind in ("skewed", "wild", "none", "one")]
+    want = [step(fp.MoePlan(T, K, E), *s) for s in sets]
+    held = [t.clone() for t in sets[0]]
+    plan = fp.MoePlan(T, K, E)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(plan, *held)
+    side = torch.cuda.Stream()
+    for k in range(8):
+        for a, b in zip(held, sets[k % 4]):
+            a.copy_(b)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            beside = step(fp.MoePlan(T, K, E), *sets[(k + 1) % 4])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[k % 4]):
+            assert torch.equal(a, b)
+        for a, b in zip(beside, want[(k + 1) % 4]):
+            assert torch.equal(a, b)
