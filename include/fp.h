@@ -15,7 +15,10 @@
  *
  * Beside the proof, the same layer's answer: the integer product with a scale
  * for each token and output channel, dense or for tokens grouped by expert, and
- * the tokens' way to their experts and back (with its gradients).
+ * the tokens' way to their experts and back (with its gradients); and what
+ * lies between and after such layers: the norm that makes their int8 rows, a
+ * mixture's layer as a whole for a few tokens, and the log probabilities that
+ * the model answers with.
  *
  * Conventions (readings where the page is silent):
  *  - rounding ties go up: Q = floor((Z + 2^(s-1)) / 2^s); R = Z - 2^s Q is taken
@@ -71,6 +74,9 @@ enum {
 #define FP_MAX_N 30       /* largest table: 2^30 entries */
 #define FP_MAX_GROUPS 256 /* groups in one grouped witness launch */
 #define FP_MAX_EXPERTS 1024           /* experts in one device sort */
+#define FP_MAX_FEW_SLOTS 1024         /* tokens times choices of a layer for few tokens */
+#define FP_MAX_NORM 16384             /* width of the rows that the norm's gradient takes */
+#define FP_MAX_TOP 32                 /* most probable tokens reported of a row of logits */
 #define FP_MAX_REQUESTS 4096          /* eq vectors in one multi-request fold */
 #define FP_MAX_FOLD_ROWS (1 << 30)    /* rows of a multi-request fold's matrix */
 #define FP_MAX_RS_LOGN 23             /* Reed-Solomon rows of up to 2^23 elements (codewords 2^24) */
@@ -197,6 +203,29 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
                             const int32_t* rows, const float* w, int32_t T, int32_t K, int32_t d, void* dO,
                             int64_t lddo, float* dw, hipStream_t stream);
 
+/* A mixture-of-experts layer for a few tokens in two launches, with the
+ * products, the row quantization and the sums of the calls it stands for
+ * (fp_scaled_linear by expert, twice, and fp_moe_combine):
+ *   a[t, k] = silu(G x_t) * (U x_t)  (gate NULL: silu(U x_t)), fp32;
+ *             silu(v) = v / (1 + exp(-v)); G, U the weights of expert ids[t, k]
+ *   Y[t, :] = sum_k weights[t, k] D a[t, k], k ascending, fp32, rounded once
+ * X [T, d] (ldx): FP_F32, FP_F16 or FP_BF16, quantized by row in the call, or
+ * FP_I8 with x_scale (device fp32 [T]; else unused). ids (device int32 or int64
+ * by id_bytes, [T, K] dense): an id outside [0, E) is a slot without an expert; a
+ * token may name an expert twice. weights: device fp32 [T, K]. gate, up: DEVICE
+ * arrays of E device pointers to each expert's weights [ff, d] from
+ * fp_witness_pack_weights, with gate_scale[e ld_gate + j] and up_scale likewise;
+ * down: of [d, ff], with down_scale. Y [T, d] (ldy) in y_dt; a token without
+ * experts gets zeros. T K <= FP_MAX_FEW_SLOTS, E <= FP_MAX_EXPERTS, d and ff in
+ * [1, FP_MAX_DIN]. ws: fp_moe_layer_workspace bytes, 256-byte aligned, contents
+ * on entry do not matter. */
+int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const float* x_scale, const void* ids, int32_t id_bytes,
+                 const float* weights, int32_t T, int32_t K, int32_t E, const int8_t* const* gate,
+                 const float* gate_scale, int64_t ld_gate, const int8_t* const* up, const float* up_scale,
+                 int64_t ld_up, const int8_t* const* down, const float* down_scale, int64_t ld_down, int32_t d,
+                 int32_t ff, fp_dtype y_dt, void* Y, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t fp_moe_layer_workspace(int32_t T, int32_t K, int32_t d, int32_t ff);
+
 /* ------------------------------------------------------------------ eq --- */
 /* E[k] = eq(r, k) for k < 2^n (r: n field elements, E: 2^n). n in [0, 30]
  * ("How fast can FlashProve go", §2: the weights of the folded row). */
@@ -292,6 +321,33 @@ int fp_scaled_linear(fp_dtype x_dt, const void* X, int64_t ldx, const int8_t* Wp
                      int32_t* Z, int64_t ldz, void* ws, size_t ws_bytes, hipStream_t stream);
 size_t fp_scaled_linear_workspace(int32_t T, int32_t d_in);
 
+/* Root-mean-square norm of rows, with what comes before and after it in a layer:
+ *   h = X[t, :] + R[t, :] (R NULL: X), in fp32; H (or NULL) gets h rounded
+ *   y = h / sqrt(mean(h^2) + eps) * w (w NULL: ones), in fp32, from h as it was
+ *       before its rounding; Y (or NULL) gets y rounded
+ *   Xq (or NULL) and scale get y as fp_quantize_rows makes them of fp32 rows
+ * X, R, H, Y [T, d] in dt (FP_F32, FP_F16 or FP_BF16), each with a leading
+ * dimension; w [d] in dt or FP_F32 (w_dt); Xq int8, scale fp32 [T]. Y or Xq must
+ * be given. eps in [1e-30, 1], d <= FP_MAX_DIN. H may be R or X, and Y may be X
+ * or R, with the same leading dimension. A row with a NaN or an infinity gives
+ * NaN where it stands (zeros beside an infinity, NaN beside a NaN) and scale NaN. */
+int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* R, int64_t ldr, fp_dtype w_dt, const void* w,
+                float eps, int32_t T, int32_t d, void* H, int64_t ldh, void* Y, int64_t ldy, int8_t* Xq, int64_t ldq,
+                float* scale, hipStream_t stream);
+
+/* The norm's gradients at H [T, d] (what it normalized; X, or the sum that
+ * fp_rms_norm left in H) from dY: with n = h / sqrt(mean(h^2) + eps),
+ *   dX = (dY w - n mean(dY w n)) / sqrt(mean(h^2) + eps) + dH  (dH NULL: 0)
+ *   dw[j] = sum_t dY[t, j] n[t, j]   (device fp32 [d], or NULL)
+ * in fp32, summed in an order fixed by T, d and the type. dX is also the gradient
+ * of X and R, dH that of the stream's later use; dX may be dY, H or dH. d <=
+ * FP_MAX_NORM. ws: fp_rms_norm_backward_workspace bytes if dw is given (else
+ * NULL), contents on entry do not matter. */
+int fp_rms_norm_backward(fp_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, fp_dtype w_dt,
+                         const void* w, float eps, const void* dH, int64_t lddh, int32_t T, int32_t d, void* dX,
+                         int64_t lddx, float* dw, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t fp_rms_norm_backward_workspace(int32_t T, int32_t d);
+
 /* fp_scaled_matmul for G groups of rows (one per expert) whose bounds only the
  * device knows: group g owns output rows [offsets[g], offsets[g + 1]) (device
  * int32 [G + 1], non-decreasing, in [0, n_rows]; fp_moe_sort writes them) and
@@ -309,6 +365,39 @@ int fp_scaled_matmul_grouped(const int8_t* X, int64_t ldx, const float* x_scale,
                              int32_t n_rows, const int8_t* const* Wp, const float* w_scale, const float* bias,
                              int64_t ld_scale, const int32_t* offsets, int32_t G, int32_t d_in, int32_t d_out,
                              fp_dtype y_dt, void* Y, int64_t ldy, int32_t* Z, int64_t ldz, hipStream_t stream);
+
+/* ---------------------------------------------------- log probabilities --- */
+/* Of every row of logits X [T, V] (ldx; FP_F32, FP_F16 or FP_BF16), the product
+ * of a model's last layer, with z = X[t, :] / temperature:
+ *   logprob[t] = log softmax(z)[tokens[t]]   (0 where the token is outside [0, V))
+ *   entropy[t] = -sum_v p_v log p_v,  p = softmax(z)  (log 0 counts nothing)
+ *   top_ids[t, j], top_logprobs[t, j], j < top: the most probable tokens, equal
+ *   logits by their index (-1 and -infinity past V)
+ *   max[t], logsum[t]: the largest logit and log sum_v exp(z_v - max z), for the
+ *   gradient
+ * all device fp32 (ids int32), dense. tokens: device int32 or int64 by id_bytes.
+ * A logit of -infinity is a token that cannot come; a row of these alone has log
+ * probability -infinity for all, entropy 0 and logsum 0. A row with a NaN or
+ * +infinity gets NaN and top ids -1. temperature in [2^-20, 2^20], top in [0,
+ * FP_MAX_TOP] (0: both NULL), V <= 2^31 - 256. Sums are fp32, in an order fixed by
+ * the sizes and the type. ws: fp_token_logprobs_workspace bytes (0 for many rows:
+ * ws may be NULL), 8-byte aligned, contents on entry do not matter. */
+int fp_token_logprobs(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
+                      int32_t id_bytes, float temperature, int32_t top, float* logprob, float* entropy, float* max,
+                      float* logsum, float* top_logprobs, int32_t* top_ids, void* ws, size_t ws_bytes,
+                      hipStream_t stream);
+size_t fp_token_logprobs_workspace(fp_dtype dt, int32_t T, int32_t V, int32_t top);
+
+/* The gradient of the logits from those of logprob and entropy (device fp32 [T];
+ * NULL: zero), with max, logsum and entropy of the forward call:
+ *   dX[t, v] = (dlogprob (1[v = token] - p_v) - dentropy p_v (log p_v + entropy))
+ *              / temperature
+ * in fp32, rounded once. A token outside [0, V) has no log probability and passes
+ * no gradient of it; a row without any token gets zeros. dX [T, V] (lddx) may be X. */
+int fp_token_logprobs_backward(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
+                               int32_t id_bytes, float temperature, const float* dlogprob, const float* dentropy,
+                               const float* max, const float* logsum, const float* entropy, void* dX, int64_t lddx,
+                               hipStream_t stream);
 
 /* --------------------------------------------------------------- folds --- */
 /* Folded row of an integer matrix ("How fast can FlashProve go", §2: the

@@ -39,7 +39,8 @@ EXPORTS = [
     "fp_commit_fold_ext_workspace", "fp_merkle_open", "fp_lookup_tree_pairs", "fp_lookup_counts_field",
     "fp_quantize_rows", "fp_scaled_matmul", "fp_scaled_linear", "fp_scaled_linear_workspace", "fp_scaled_matmul_grouped",
     "fp_moe_sort", "fp_moe_sort_workspace", "fp_moe_permute", "fp_moe_dispatch", "fp_moe_combine",
-    "fp_moe_combine_backward",
+    "fp_moe_combine_backward", "fp_moe_layer", "fp_moe_layer_workspace", "fp_rms_norm", "fp_rms_norm_backward",
+    "fp_rms_norm_backward_workspace", "fp_token_logprobs", "fp_token_logprobs_workspace", "fp_token_logprobs_backward",
 ]
 
 _lib = None
@@ -104,6 +105,7 @@ def lib():
             raise FPError("libfp.so is not built (run __graft_entry__.build()): %s" % LIB_PATH)
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_uint64
+        f32 = ctypes.c_float
         sig = {
             "fp_last_error": (ctypes.c_char_p, []),
             "fp_witness_linear": (ctypes.c_int, [vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp]),
@@ -189,6 +191,19 @@ def lib():
             "fp_moe_combine": (ctypes.c_int, [i32, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp]),
             "fp_moe_combine_backward": (ctypes.c_int, [i32, vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp,
                                                        vp]),
+            "fp_moe_layer": (ctypes.c_int, [i32, vp, i64, vp, vp, i32, vp, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp,
+                                            i64, i32, i32, i32, vp, i64, vp, sz, vp]),
+            "fp_moe_layer_workspace": (sz, [i32, i32, i32, i32]),
+            "fp_rms_norm": (ctypes.c_int, [i32, vp, i64, vp, i64, i32, vp, f32, i32, i32, vp, i64, vp, i64, vp, i64, vp,
+                                           vp]),
+            "fp_rms_norm_backward": (ctypes.c_int, [i32, vp, i64, vp, i64, i32, vp, f32, vp, i64, i32, i32, vp, i64, vp, vp,
+                                                    sz, vp]),
+            "fp_rms_norm_backward_workspace": (sz, [i32, i32]),
+            "fp_token_logprobs": (ctypes.c_int, [i32, vp, i64, i32, i32, vp, i32, f32, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                                 vp]),
+            "fp_token_logprobs_workspace": (sz, [i32, i32, i32, i32]),
+            "fp_token_logprobs_backward": (ctypes.c_int, [i32, vp, i64, i32, i32, vp, i32, f32, vp, vp, vp, vp, vp, vp, i64,
+                                                          vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -761,6 +776,102 @@ def scaled_linear(X, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=None
     return out
 
 
+# ------------------------------------------------------------------- norms --
+def _norm_args(X, weight, name: str):
+    """Rows' type and width, the weights' type and address."""
+    if X.dim() != 2:
+        raise ValueError("%s: shape %s, expected two dimensions" % (name, tuple(X.shape)))
+    T, d = X.shape
+    dt = _float_dt(X.dtype, name)
+    if weight is None:
+        return T, d, dt, dt, 0
+    if weight.dtype is not X.dtype and weight.dtype is not torch.float32:
+        raise ValueError("weight: %s, expected %s or float32" % (weight.dtype, X.dtype))
+    _vector(weight, weight.dtype, (d,), "weight")
+    return T, d, dt, _FLOATS[weight.dtype], weight.data_ptr()
+
+
+def _stream_rows(X, residual, residual_out):
+    """The residual's address and leading dimension, and where the sum goes (made if None and there is a residual)."""
+    T, d = X.shape
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out: no residual to add")
+        return 0, d, None, 0, d
+    ldr = _matrix(residual, X.dtype, T, d, "residual")
+    if residual_out is None:
+        residual_out = torch.empty((T, d), dtype=X.dtype, device=X.device)
+    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), _matrix(residual_out, X.dtype, T, d, "residual_out")
+
+
+def rms_norm(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None):
+    """Y = h / sqrt(mean(h^2) + eps) * weight for the rows h of X [T, d] (float32, float16 or bfloat16), in X's type; weight
+    [d] in X's type or float32 (None: ones). With a ``residual`` h = X + residual, and (Y, H) is returned, H being the sum
+    in X's type (``residual_out``, which may be the residual itself or X); the norm is of the sum before that rounding.
+    Sums in fp32. The gradient is rms_norm_backward; no graph is recorded, and tensors that require a gradient are refused
+    unless under torch.no_grad."""
+    _no_graph("rms_norm_backward", X, weight, residual)
+    T, d, dt, w_dt, w = _norm_args(X, weight, "X")
+    ldx = _matrix(X, None, T, d, "X")
+    r, ldr, H, h, ldh = _stream_rows(X, residual, residual_out)
+    if out is None:
+        out = torch.empty((T, d), dtype=X.dtype, device=X.device)
+    ldy = _matrix(out, X.dtype, T, d, "out")
+    st = _here(X, weight, residual, H, out)
+    _check(lib().fp_rms_norm(dt, X.data_ptr(), ldx, r, ldr, w_dt, w, eps, T, d, h, ldh, out.data_ptr(), ldy, 0, d, 0, st),
+           "fp_rms_norm")
+    return out if H is None else (out, H)
+
+
+def rms_norm_quantize(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None, scale=None, Y=None):
+    """(Xq, scale), with a ``residual`` (Xq, scale, H): quantize_rows of rms_norm's fp32 rows, for scaled_matmul or
+    moe_layer. ``Y`` (X's type) also receives the rows themselves, which a router reads. The int8 rows have no gradient."""
+    _no_graph("rms_norm_backward", X, weight, residual)
+    T, d, dt, w_dt, w = _norm_args(X, weight, "X")
+    ldx = _matrix(X, None, T, d, "X")
+    r, ldr, H, h, ldh = _stream_rows(X, residual, residual_out)
+    if out is None:
+        out = torch.empty((T, (d + 15) // 16 * 16), dtype=torch.int8, device=X.device)
+        if d % 16:
+            out = out[:, :d]
+    ldq = _matrix(out, torch.int8, T, d, "out")
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=X.device)
+    else:
+        _vector(scale, torch.float32, (T,), "scale")
+    y, ldy = (0, d) if Y is None else (Y.data_ptr(), _matrix(Y, X.dtype, T, d, "Y"))
+    st = _here(X, weight, residual, H, out, scale, Y)
+    _check(lib().fp_rms_norm(dt, X.data_ptr(), ldx, r, ldr, w_dt, w, eps, T, d, h, ldh, y, ldy, out.data_ptr(), ldq,
+                             scale.data_ptr(), st), "fp_rms_norm")
+    return (out, scale) if H is None else (out, scale, H)
+
+
+def rms_norm_backward(dY, H, weight, eps: float = 1e-5, dH=None, out=None, dw=None):
+    """(dX, dw), the gradients of rms_norm at H [T, d] (its X, or the sum it returned) from dY: dX [T, d] in H's type, of X
+    and of the residual alike, with ``dH``, the gradient of H's other uses, added; dw float32 [d] (None without weights).
+    d is at most 16384."""
+    T, d, dt, w_dt, w = _norm_args(H, weight, "H")
+    ldh, lddy = _matrix(H, None, T, d, "H"), _matrix(dY, H.dtype, T, d, "dY")
+    lddh = d if dH is None else _matrix(dH, H.dtype, T, d, "dH")
+    if out is None:
+        out = torch.empty((T, d), dtype=H.dtype, device=H.device)
+    lddx = _matrix(out, H.dtype, T, d, "out")
+    if weight is None:
+        if dw is not None:
+            raise ValueError("dw: there are no weights")
+    elif dw is None:
+        dw = torch.empty(d, dtype=torch.float32, device=H.device)
+    else:
+        _vector(dw, torch.float32, (d,), "dw")
+    st = _here(dY, H, weight, dH, out, dw)
+    nbytes = 0 if dw is None else lib().fp_rms_norm_backward_workspace(T, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=H.device)
+    _check(lib().fp_rms_norm_backward(dt, dY.data_ptr(), lddy, H.data_ptr(), ldh, w_dt, w, eps,
+                                      0 if dH is None else dH.data_ptr(), lddh, T, d, out.data_ptr(), lddx,
+                                      0 if dw is None else dw.data_ptr(), ws.data_ptr(), nbytes, st), "fp_rms_norm_backward")
+    return out, dw
+
+
 class PackedExperts:
     """The packed weights of G experts of one shape (pack_experts): ``weights`` holds each one's PackedWeights."""
 
@@ -778,6 +889,8 @@ class PackedExperts:
         # (first expert, how many, their addresses in ptrs): a launch takes MAX_GROUPS
         counts = [(g, min(MAX_GROUPS, len(weights) - g)) for g in range(0, len(weights), MAX_GROUPS)]
         self.parts = [(g, n, (ctypes.c_void_p * n).from_buffer(self.ptrs, g * ctypes.sizeof(ctypes.c_void_p))) for g, n in counts]
+        # the addresses on the device, for calls whose experts only the device knows
+        self.table = torch.tensor([w.data.data_ptr() for w in weights], dtype=torch.int64).to(self.device)
 
     def __len__(self):
         return len(self.weights)
@@ -964,6 +1077,135 @@ def moe_combine_backward(dY, O, plan: MoePlan, weights, dO=None, dw=None):
                                          weights.data_ptr(), T, K, d, dO.data_ptr(), ldo, dw.data_ptr(), st),
            "fp_moe_combine_backward")
     return dO, dw
+
+
+def _expert_scales(We, scale, shape, name: str):
+    """Check an expert map and its scales; their addresses and the scales' leading dimension."""
+    if (We.d_out, We.d_in) != shape:
+        raise ValueError("%s: experts of %d -> %d, expected %d -> %d" % (name, We.d_in, We.d_out, shape[1], shape[0]))
+    return We.table.data_ptr(), scale.data_ptr(), _matrix(scale, torch.float32, len(We.weights), shape[0], name + "_scale")
+
+
+def moe_layer(X, ids, weights, up: PackedExperts, up_scale, down: PackedExperts, down_scale, gate: PackedExperts | None = None,
+              gate_scale=None, x_scale=None, out=None, dtype=None):
+    """Y [T, d] = sum_k weights[t, k] Down(silu(Gate x_t) * Up x_t) by the experts ids[t, k] (without a gate: silu(Up x_t)),
+    for a few tokens (T K at most 1024), in two launches: the answer of the same layer strung together from scaled_linear's
+    products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8 with ``x_scale`` (rms_norm_quantize's
+    rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a slot without an expert; weights float32
+    [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with float32 scales [E, outputs]. Y is in
+    ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: an X or weights that require one are refused
+    unless under torch.no_grad."""
+    if (X.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("X or weights require a gradient, which this layer does not have: train through moe_dispatch and "
+                         "moe_combine, or detach them")
+    if X.dim() != 2:
+        raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
+    T, d = X.shape
+    if X.dtype is torch.int8:
+        if x_scale is None:
+            raise ValueError("x_scale: int8 rows have scales")
+        _vector(x_scale, torch.float32, (T,), "x_scale")
+        x_dt = FP_I8
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale: %s rows have none" % X.dtype)
+        x_dt = _float_dt(X.dtype, "X")
+    ldx = _matrix(X, None, T, d, "X")
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids: %s %s, expected contiguous int32 or int64 (%d, K)" % (ids.dtype, tuple(ids.shape), T))
+    K, E, ff = ids.shape[1], len(up.weights), up.d_out
+    _vector(weights, torch.float32, (T, K), "weights")
+    if (gate is None) != (gate_scale is None):
+        raise ValueError("gate and gate_scale come together")
+    if len(down.weights) != E or (gate is not None and len(gate.weights) != E):
+        raise ValueError("maps of different numbers of experts")
+    u, us, ldu = _expert_scales(up, up_scale, (ff, d), "up")
+    dn, ds, ldd = _expert_scales(down, down_scale, (d, ff), "down")
+    g, gs, ldg = (0, 0, ff) if gate is None else _expert_scales(gate, gate_scale, (ff, d), "gate")
+    if out is None:
+        dtype = dtype or (torch.bfloat16 if x_dt == FP_I8 else X.dtype)
+        _float_dt(dtype, "out")
+        out = torch.empty((T, d), dtype=dtype, device=X.device)
+    ldy = _matrix(out, None, T, d, "out")
+    y_dt = _float_dt(out.dtype, "out")
+    st = _here(X, x_scale, ids, weights, up.table, up_scale, down.table, down_scale, gate and gate.table, gate_scale, out)
+    nbytes = lib().fp_moe_layer_workspace(T, K, d, ff)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    _check(lib().fp_moe_layer(x_dt, X.data_ptr(), ldx, 0 if x_scale is None else x_scale.data_ptr(), ids.data_ptr(),
+                              ids.element_size(), weights.data_ptr(), T, K, E, g, gs, ldg, u, us, ldu, dn, ds, ldd, d, ff,
+                              y_dt, out.data_ptr(), ldy, ws.data_ptr(), nbytes, st), "fp_moe_layer")
+    return out
+
+
+# ------------------------------------------------------- log probabilities --
+class TokenLogprobs:
+    """What token_logprobs says of T rows of logits: ``logprob`` and ``entropy`` float32 [T], ``top_logprobs`` float32 and
+    ``top_ids`` int32 [T, top], and ``max`` and ``logsum`` float32 [T], which the gradient reads. A program that asks at every
+    step may keep one."""
+
+    def __init__(self, T: int, top: int = 0, device=None):
+        if T < 0 or top < 0:
+            raise ValueError("TokenLogprobs: T=%d top=%d" % (T, top))
+        self.T, self.top = T, top
+        buf = torch.empty(T * (4 + 2 * top), dtype=torch.float32, device=device or _dev())
+        self.logprob, self.entropy, self.max, self.logsum = (buf[i * T:(i + 1) * T] for i in range(4))
+        self.top_logprobs = buf[4 * T:(4 + top) * T].view(T, top)
+        self.top_ids = buf[(4 + top) * T:].view(torch.int32).view(T, top)
+        self.buf = buf
+        self.ptrs = tuple(t.data_ptr() for t in (self.logprob, self.entropy, self.max, self.logsum)) + (
+            (self.top_logprobs.data_ptr(), self.top_ids.data_ptr()) if top else (0, 0))
+
+
+def _logit_args(logits, tokens):
+    if logits.dim() != 2:
+        raise ValueError("logits: shape %s, expected two dimensions" % (tuple(logits.shape),))
+    T, V = logits.shape
+    dt = _float_dt(logits.dtype, "logits")
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise ValueError("tokens: %s, expected int32 or int64" % tokens.dtype)
+    _vector(tokens, tokens.dtype, (T,), "tokens")
+    return T, V, dt, _matrix(logits, None, T, V, "logits")
+
+
+def token_logprobs(logits, tokens, temperature: float = 1.0, top: int = 0, out: TokenLogprobs | None = None) -> TokenLogprobs:
+    """Of every row of logits [T, V] (float32, float16 or bfloat16), divided by the temperature: the log probability of
+    tokens[t] (int32 or int64 on the device; one outside [0, V) is padding and gets 0), the entropy, and the ``top`` most
+    probable tokens (at most 32; equal logits by their index). Logits of -infinity are tokens that cannot come; a row of
+    these alone has log probability -infinity and entropy 0, one with a NaN or +infinity NaN and top ids -1. The gradient
+    is token_logprobs_backward; no graph is recorded, and logits that require a gradient are refused unless under
+    torch.no_grad."""
+    _no_graph("token_logprobs_backward", logits)
+    T, V, dt, ldx = _logit_args(logits, tokens)
+    if out is None:
+        out = TokenLogprobs(T, top, logits.device)
+    elif (out.T, out.top) != (T, top):
+        raise ValueError("out: for T=%d top=%d, the call has T=%d top=%d" % (out.T, out.top, T, top))
+    st = _here(logits, tokens, out.buf)
+    nbytes = lib().fp_token_logprobs_workspace(dt, T, V, top)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=logits.device) if nbytes else None
+    _check(lib().fp_token_logprobs(dt, logits.data_ptr(), ldx, T, V, tokens.data_ptr(), tokens.element_size(), temperature,
+                                   top, *out.ptrs, ws.data_ptr() if nbytes else 0, nbytes, st), "fp_token_logprobs")
+    return out
+
+
+def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lp: TokenLogprobs, temperature: float = 1.0, out=None):
+    """dlogits [T, V] in the logits' type, from the gradients of lp.logprob and lp.entropy (float32 [T]; None: zero), lp
+    being what token_logprobs said of the same logits, tokens and temperature. ``out`` may be the logits themselves."""
+    T, V, dt, ldx = _logit_args(logits, tokens)
+    for g, name in ((dlogprob, "dlogprob"), (dentropy, "dentropy")):
+        if g is not None:
+            _vector(g, torch.float32, (T,), name)
+    if lp.T != T:
+        raise ValueError("lp: for T=%d, the call has T=%d" % (lp.T, T))
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    lddx = _matrix(out, logits.dtype, T, V, "out")
+    st = _here(dlogprob, dentropy, logits, tokens, lp.buf, out)
+    _check(lib().fp_token_logprobs_backward(dt, logits.data_ptr(), ldx, T, V, tokens.data_ptr(), tokens.element_size(),
+                                            temperature, 0 if dlogprob is None else dlogprob.data_ptr(),
+                                            0 if dentropy is None else dentropy.data_ptr(), lp.ptrs[2], lp.ptrs[3],
+                                            lp.ptrs[1], out.data_ptr(), lddx, st), "fp_token_logprobs_backward")
+    return out
 
 
 # ----------------------------------------------------------------------- eq --

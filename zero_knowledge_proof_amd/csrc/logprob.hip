@@ -1,0 +1,506 @@
+// logprob.hip - from rows of logits the log probability of a given token, the
+// row's entropy and its most probable tokens, and the gradient of the first two.
+//
+//   z_v = x_v / temperature,  S = sum_v exp(z_v - max z),  log p_v = z_v - max z - log S
+//   H = -sum_v p_v log p_v = log S - sum_v (z_v - max z) exp(z_v - max z) / S
+//   dx_v = (dlogprob (1[v = token] - p_v) - dentropy p_v (log p_v + H)) / temperature
+// in fp32, one pass over a row with a running maximum. A token of logit -infinity
+// has p = 0 and adds nothing. A row of these alone has no distribution: every log
+// probability is -infinity, H and the gradient are 0. A row with a NaN or +infinity
+// has NaN everywhere, and -1 for its top tokens. Equal logits rank by their index.
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include "common.hpp"
+#include "scaled_dev.hpp"
+
+namespace {
+
+using sdev::load_elem;
+using sdev::v4i;
+
+constexpr int NT = 256;
+constexpr int CAP = 1024;  // candidates in LDS; also the most that the parts of a row hand over
+constexpr float LOG2E = 1.44269504088896340736f;
+
+struct LogArgs {
+  const void* X;
+  int64_t ldx;
+  int32_t T, V;
+  const void* tokens;
+  int32_t wide;  // tokens are int64
+  float inv_t;   // 1 / temperature
+  int32_t top;
+  int32_t splits, per;  // parts of a row, and chunks of each
+  float *logprob, *entropy, *max, *logsum, *top_lp;
+  int32_t* top_ids;
+  float* stats;    // [T][splits][3]: max, S, sum (x - max) exp: with splits > 1
+  uint64_t* keys;  // [T][splits][top]
+};
+
+// Keys order logits, the lower index first among equals: the value's bits made
+// monotone in the high half, the index's complement in the low one. 0 is none.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);  // one zero
+  return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
+__device__ __forceinline__ uint64_t make_key(float x, uint32_t idx) { return (uint64_t)ordered(x) << 32 | (0xFFFFFFFFu - idx); }
+__device__ __forceinline__ float key_value(uint64_t k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xFFFFFFFFu - (uint32_t)k; }
+
+// Softmax statistics of a part: m the maximum, s = sum exp((x - m) k), u = sum
+// (x - m) exp((x - m) k).
+struct Stats {
+  float m, s, u;
+};
+// `a` taken to the maximum m >= a.m.
+__device__ __forceinline__ Stats at_max(const Stats& a, float m, float k2) {
+  const float d = a.m - m;  // -infinity where a part has nothing: then s = u = 0 (unless a NaN came)
+  const float c = a.m == m ? 1.0f : __builtin_amdgcn_exp2f(d * k2);
+  return Stats{m, a.s * c, a.m == m ? a.u : c * (a.u + fmaxf(d, -1e30f) * a.s)};
+}
+// All threads' statistics as one, to every thread.
+__device__ __forceinline__ Stats block_stats(Stats v, float k2, float (*red)[3]) {
+  float m = v.m;
+#pragma unroll
+  for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+  v = at_max(v, m, k2);
+#pragma unroll
+  for (int x = 32; x; x >>= 1) {
+    v.s += __shfl_xor(v.s, x, 64);
+    v.u += __shfl_xor(v.u, x, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6][0] = v.m;
+    red[threadIdx.x >> 6][1] = v.s;
+    red[threadIdx.x >> 6][2] = v.u;
+  }
+  __syncthreads();
+  m = red[0][0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[w][0]);
+  Stats all{m, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    const Stats p = at_max(Stats{red[w][0], red[w][1], red[w][2]}, m, k2);
+    all.s += p.s;
+    all.u += p.u;
+  }
+  __syncthreads();
+  return all;
+}
+
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) { return fpi::shfl_xor_u64(v, m); }
+
+// The candidates of a row's part: distinct keys in LDS.
+struct Candidates {
+  uint64_t key[CAP], best[FP_MAX_TOP], group[NT / 4], tau;
+  int n;
+};
+
+// The k greatest of the n <= CAP keys, to the front of `key` in descending
+// order, by counting for each how many are greater. Returns how many there are.
+__device__ __forceinline__ int keep_top(Candidates& c, int n, int k) {
+  if ((int)threadIdx.x < k) c.best[threadIdx.x] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint64_t mine = c.key[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += c.key[j] > mine;
+    if (rank < k) c.best[rank] = mine;
+  }
+  __syncthreads();
+  const int have = min(n, k);
+  if ((int)threadIdx.x < have) c.key[threadIdx.x] = c.best[threadIdx.x];
+  if (threadIdx.x == 0) c.n = have;
+  __syncthreads();
+  return have;
+}
+
+// What a row's statistics and its sorted keys say, written down.
+template <typename E>
+__device__ __forceinline__ void finish_row(const LogArgs& a, int64_t t, const Stats& st, const uint64_t* best, int have) {
+  const bool bad = st.s != st.s, empty = st.s == 0.f;
+  const float log_s = empty ? 0.f : logf(st.s);
+  auto log_p = [&](float x) { return empty ? -__builtin_inff() : (x - st.m) * a.inv_t - log_s; };
+  if (threadIdx.x == 0) {
+    const int64_t tok = a.wide ? ((const int64_t*)a.tokens)[t] : ((const int32_t*)a.tokens)[t];
+    a.logprob[t] = tok >= 0 && tok < a.V ? log_p(sdev::elem_float((const E*)a.X + t * a.ldx + tok)) : 0.f;
+    const float h = empty ? 0.f : log_s - a.inv_t * (st.u / st.s);
+    a.entropy[t] = h < 0.f ? 0.f : h;
+    a.max[t] = st.m;
+    a.logsum[t] = log_s;
+  }
+  if ((int)threadIdx.x < a.top) {
+    const uint64_t k = (int)threadIdx.x < have ? best[threadIdx.x] : 0;
+    const bool none = bad || k == 0 || key_index(k) >= (uint32_t)a.V;
+    a.top_ids[t * a.top + threadIdx.x] = none ? -1 : (int32_t)key_index(k);
+    a.top_lp[t * a.top + threadIdx.x] = bad ? __builtin_nanf("") : (none ? -__builtin_inff() : log_p(key_value(k)));
+  }
+}
+
+// A workgroup to a row's part, a chunk of NV vectors a thread at a time.
+template <typename E, int NV>
+__global__ __launch_bounds__(NT) void logprob_kernel(LogArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), CH = NT * NV * EV;
+  __shared__ Candidates cand;
+  __shared__ float red[NT / 64][3];
+  const int tid = threadIdx.x;
+  const float k2 = a.inv_t * LOG2E;
+  const int64_t tasks = (int64_t)a.T * a.splits;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t t = task / a.splits;
+    const int part = (int)(task % a.splits);
+    const E* row = (const E*)a.X + t * a.ldx;
+    const int64_t lo = (int64_t)part * a.per * CH;
+    const int64_t hi = min(lo + (int64_t)a.per * CH, (int64_t)a.V);
+    Stats st{-__builtin_inff(), 0.f, 0.f};
+    int n = 0;  // candidates, and whether they hold `top` sorted ones already
+    bool full = false;
+    uint64_t kth = 0;
+    if (a.top) {
+      __syncthreads();
+      if (tid == 0) cand.n = 0;
+      __syncthreads();
+    }
+    for (int64_t base = lo; base < hi; base += CH) {
+      v4i raw[NV];
+      if (base + CH <= a.V) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) raw[v] = sdev::load16u(row + base + (v * NT + tid) * EV, EV);
+      } else {  // past the row: -infinity
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int64_t left = a.V - (base + (v * NT + tid) * EV);
+          raw[v] = v4i{0, 0, 0, 0};
+          if (left > 0) raw[v] = sdev::load16u(row + base + (v * NT + tid) * EV, left);
+          const uint32_t none = sdev::Out<E>::bits(-__builtin_inff());
+#pragma unroll
+          for (int e = 0; e < EV; ++e)
+            if (e >= left) {
+              if constexpr (sizeof(E) == 4) raw[v][e] = (int)none;
+              else raw[v][e / 2] = e % 2 ? (int)(((uint32_t)raw[v][e / 2] & 0xFFFFu) | none << 16) : (int)(((uint32_t)raw[v][e / 2] & 0xFFFF0000u) | none);
+            }
+        }
+      }
+      float mt = -__builtin_inff();
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < EV; ++e) mt = fmaxf(mt, load_elem<E>(raw[v], e));
+      if (mt > st.m) st = at_max(st, mt, k2);
+      const float m0 = st.m == -__builtin_inff() ? 0.f : st.m;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          const float d = load_elem<E>(raw[v], e) - m0, p = __builtin_amdgcn_exp2f(d * k2);
+          st.s += p;
+          st.u = __builtin_fmaf(fmaxf(d, -1e30f), p, st.u);
+        }
+      if (!a.top) continue;
+      // ---- candidates for the top
+      auto index = [&](int v, int e) { return (uint32_t)(base + (v * NT + tid) * EV + e); };
+      // a key that at least `top` of the chunk's reach: of the maxima of 64 groups of four threads
+      auto group_key = [&]() -> uint64_t {
+        uint64_t best = 0;
+#pragma unroll
+        for (int v = NV - 1; v >= 0; --v)
+#pragma unroll
+          for (int e = EV - 1; e >= 0; --e)
+            if (load_elem<E>(raw[v], e) == mt) best = make_key(mt, index(v, e));
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+          const uint64_t o = shfl_xor64(best, x);
+          best = o > best ? o : best;
+        }
+        if (tid == 0) cand.tau = 0;
+        if (tid % 4 == 0) cand.group[tid / 4] = best;
+        __syncthreads();
+        if (tid < 64) {
+          const uint64_t mine = cand.group[tid];
+          int rank = 0;
+#pragma unroll 8
+          for (int i = 0; i < 64; ++i) rank += cand.group[i] > mine;
+          if (rank == a.top - 1) cand.tau = mine;
+        }
+        __syncthreads();
+        return cand.tau;
+      };
+      auto gather = [&](uint64_t lim) {
+        const float least = lim ? key_value(lim) : -__builtin_inff();
+        if (mt >= least) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+              const float x = load_elem<E>(raw[v], e);
+              if (x >= least) {
+                const uint64_t k = make_key(x, index(v, e));
+                if (k >= lim) {
+                  const int at = atomicAdd(&cand.n, 1);
+                  if (at < CAP) cand.key[at] = k;
+                }
+              }
+            }
+        }
+        __syncthreads();
+        const int all = cand.n;
+        __syncthreads();  // the next candidates come after every thread has read it
+        return all;
+      };
+      uint64_t lim = full ? kth + 1 : group_key();
+      int got = gather(lim);
+      if (got > CAP) {  // uniform
+        n = keep_top(cand, n, a.top);
+        if (n == a.top) lim = max(lim, cand.key[n - 1] + 1);
+        lim = max(lim, group_key());
+        got = gather(lim);
+        if (got > CAP) {  // one at a time, from the greatest down
+          uint64_t below = ~0ull;
+          got = n;
+          for (int j = 0; j < a.top; ++j) {
+            uint64_t best = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+              for (int e = 0; e < EV; ++e) {
+                const float x = load_elem<E>(raw[v], e);
+                const uint64_t k = make_key(x, index(v, e));
+                if (x == x && k < below && k > best) best = k;
+              }
+#pragma unroll
+            for (int x = 32; x; x >>= 1) {
+              const uint64_t o = shfl_xor64(best, x);
+              best = o > best ? o : best;
+            }
+            __syncthreads();
+            if ((tid & 63) == 0) cand.group[tid >> 6] = best;
+            __syncthreads();
+            best = 0;
+            for (int w = 0; w < NT / 64; ++w) best = max(best, cand.group[w]);
+            if (best < lim || best == 0) break;  // uniform
+            if (tid == 0) cand.key[got] = best;
+            ++got;
+            below = best;
+          }
+          __syncthreads();
+          if (tid == 0) cand.n = got;
+          __syncthreads();
+        }
+      }
+      n = got;
+      if (!full || n > CAP / 2) {
+        n = keep_top(cand, n, a.top);
+        full = n == a.top;
+        if (full) kth = cand.key[n - 1];
+      }
+    }
+    if (a.top) n = keep_top(cand, n, a.top);
+    st = block_stats(st, k2, red);
+    if (a.splits == 1) {
+      finish_row<E>(a, t, st, cand.key, n);
+    } else {
+      if (tid == 0) {
+        a.stats[task * 3] = st.m;
+        a.stats[task * 3 + 1] = st.s;
+        a.stats[task * 3 + 2] = st.u;
+      }
+      if (tid < a.top) a.keys[task * a.top + tid] = tid < n ? cand.key[tid] : 0;
+    }
+  }
+}
+
+// A row's parts joined.
+template <typename E>
+__global__ __launch_bounds__(NT) void logprob_join_kernel(LogArgs a) {
+  __shared__ Candidates cand;
+  __shared__ float red[NT / 64][3];
+  const int tid = threadIdx.x;
+  const float k2 = a.inv_t * LOG2E;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    Stats st{-__builtin_inff(), 0.f, 0.f};
+    if (tid < a.splits) {
+      const float* p = a.stats + (t * a.splits + tid) * 3;
+      st = Stats{p[0], p[1], p[2]};
+    }
+    int n = a.splits * a.top;  // at most CAP
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) cand.key[i] = a.keys[t * n + i];
+    if (n) n = keep_top(cand, n, a.top);
+    st = block_stats(st, k2, red);
+    finish_row<E>(a, t, st, cand.key, n);
+  }
+}
+
+// ---- the gradient -----------------------------------------------------------
+struct LogBwdArgs {
+  const void* X;
+  int64_t ldx;
+  int32_t T, V;
+  const void* tokens;
+  int32_t wide;
+  float inv_t;
+  const float *dlogprob, *dentropy, *max, *logsum, *entropy;  // dlogprob, dentropy: NULL is zero
+  void* dX;
+  int64_t lddx;
+  int32_t chunks;
+};
+
+// A workgroup to a chunk of a row, NV vectors a thread.
+template <typename E, int NV>
+__global__ __launch_bounds__(NT) void logprob_backward_kernel(LogBwdArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), CH = NT * NV * EV;
+  typedef typename sdev::AnyVec<sizeof(E)>::type Vec;
+  const int64_t tasks = (int64_t)a.T * a.chunks;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t t = task / a.chunks, base = (task % a.chunks) * CH;
+    const E* x = (const E*)a.X + t * a.ldx;
+    E* y = (E*)a.dX + t * a.lddx;
+    v4i raw[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t at = base + (v * NT + (int)threadIdx.x) * EV;
+      raw[v] = v4i{0, 0, 0, 0};
+      if (at < a.V) raw[v] = sdev::load16u(x + at, a.V - at);
+    }
+    const float m = a.max[t], log_s = a.logsum[t], h = a.entropy[t];
+    const int64_t tok = a.wide ? ((const int64_t*)a.tokens)[t] : ((const int32_t*)a.tokens)[t];
+    const bool empty = m == -__builtin_inff() && log_s == 0.f;
+    const float dl = a.dlogprob && tok >= 0 && tok < a.V ? a.dlogprob[t] * a.inv_t : 0.f;
+    const float dh = a.dentropy ? a.dentropy[t] * a.inv_t : 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t at = base + (v * NT + (int)threadIdx.x) * EV;
+      float d[EV];
+#pragma unroll
+      for (int e = 0; e < EV; ++e) {
+        const float lp = fmaxf((load_elem<E>(raw[v], e) - m) * a.inv_t - log_s, -1e30f);
+        const float p = __builtin_amdgcn_exp2f(lp * LOG2E);
+        d[e] = dl * ((at + e == tok ? 1.f : 0.f) - p) - dh * p * (lp + h);
+        if (empty) d[e] = 0.f;
+      }
+      const v4i w = sdev::pack16<E>(d);
+      if (at + EV <= a.V) {
+        *(Vec*)(y + at) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < EV; ++e)
+          if (at + e < a.V) sdev::store_elem(y + at + e, d[e]);
+      }
+    }
+  }
+}
+
+int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+
+struct Plan {
+  int nv, splits, per;
+};
+// Rows that fill the GPU are not cut; fewer are, into up to 32 parts.
+Plan plan_rows(fp_dtype dt, int32_t T, int32_t V) {
+  const int64_t ev = 16 / elem_bytes(dt);
+  auto chunks = [&](int nv) { return ((int64_t)V + NT * nv * ev - 1) / (NT * nv * ev); };
+  Plan p{8, 1, 1};
+  if (V <= NT * 2 * ev || T * chunks(8) < 512) p.nv = 2;
+  const int64_t c = chunks(p.nv);
+  if (c == 0 || T == 0) return p;
+  int64_t s = (1024 + T - 1) / T;
+  s = s < c ? s : c;
+  s = s < 32 ? s : 32;
+  p.per = (int)((c + s - 1) / s);
+  p.splits = (int)((c + p.per - 1) / p.per);
+  return p;
+}
+
+int check_rows(const char* fn, fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens, int32_t id_bytes,
+               float temperature) {
+  if (T < 0 || V < 0) return fpi::fail(FP_EARG, "%s: negative size", fn);
+  const int eb = elem_bytes(dt);
+  if (!eb) return fpi::fail(FP_EARG, "%s: unknown type %d", fn, (int)dt);
+  if (V > 0x7FFFFF00) return fpi::fail(FP_ESHAPE, "%s: V=%d", fn, V);
+  if (ldx < V) return fpi::fail(FP_ESHAPE, "%s: leading dimension too small", fn);
+  if (id_bytes != 4 && id_bytes != 8) return fpi::fail(FP_EARG, "%s: tokens of %d bytes", fn, id_bytes);
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return fpi::fail(FP_EARG, "%s: temperature=%g outside [2^-20, 2^20]", fn, (double)temperature);
+  if (T > 0 && ((V > 0 && !X) || !tokens)) return fpi::fail(FP_EARG, "%s: null pointer", fn);
+  if ((uintptr_t)X % eb || (uintptr_t)tokens % id_bytes) return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  return FP_OK;
+}
+
+template <typename E>
+int launch_rows(const LogArgs& a, int nv, hipStream_t st) {
+  const int64_t tasks = (int64_t)a.T * a.splits;
+  const dim3 grid((unsigned)(tasks < (1 << 20) ? tasks : 1 << 20));
+  if (nv == 8) logprob_kernel<E, 8><<<grid, dim3(NT), 0, st>>>(a);
+  else logprob_kernel<E, 2><<<grid, dim3(NT), 0, st>>>(a);
+  int rc = fpi::check_launch("logprob_kernel");
+  if (rc || a.splits == 1) return rc;
+  logprob_join_kernel<E><<<dim3((unsigned)(a.T < (1 << 20) ? a.T : 1 << 20)), dim3(NT), 0, st>>>(a);
+  return fpi::check_launch("logprob_join_kernel");
+}
+
+template <typename E>
+void launch_backward(LogBwdArgs a, hipStream_t st) {
+  constexpr int NV = 4, CH = NT * NV * 16 / (int)sizeof(E);
+  a.chunks = (int32_t)(((int64_t)a.V + CH - 1) / CH);
+  const int64_t tasks = (int64_t)a.T * a.chunks;
+  logprob_backward_kernel<E, NV><<<dim3((unsigned)(tasks < (1 << 20) ? tasks : 1 << 20)), dim3(NT), 0, st>>>(a);
+}
+
+}  // namespace
+
+extern "C" size_t fp_token_logprobs_workspace(fp_dtype dt, int32_t T, int32_t V, int32_t top) {
+  if (T < 0 || V < 0 || top < 0 || top > FP_MAX_TOP || !elem_bytes(dt)) return 0;
+  const Plan p = plan_rows(dt, T, V);
+  return p.splits == 1 ? 0 : (size_t)T * p.splits * ((size_t)top * 8 + 12);
+}
+
+extern "C" int fp_token_logprobs(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
+                                 int32_t id_bytes, float temperature, int32_t top, float* logprob, float* entropy, float* max,
+                                 float* logsum, float* top_logprobs, int32_t* top_ids, void* ws, size_t ws_bytes,
+                                 hipStream_t stream) {
+  const char* fn = "fp_token_logprobs";
+  int rc = check_rows(fn, dt, X, ldx, T, V, tokens, id_bytes, temperature);
+  if (rc) return rc;
+  if (top < 0 || top > FP_MAX_TOP) return fpi::fail(FP_EARG, "%s: top=%d outside [0, %d]", fn, top, FP_MAX_TOP);
+  if (T > 0 && (!logprob || !entropy || !max || !logsum || (top && (!top_logprobs || !top_ids))))
+    return fpi::fail(FP_EARG, "%s: null pointer", fn);
+  if (((uintptr_t)logprob | (uintptr_t)entropy | (uintptr_t)max | (uintptr_t)logsum | (uintptr_t)top_logprobs | (uintptr_t)top_ids) % 4)
+    return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  const size_t need = fp_token_logprobs_workspace(dt, T, V, top);
+  if (need && (!ws || ws_bytes < need)) return fpi::fail(FP_EWORKSPACE, "%s: workspace %zu < %zu", fn, ws ? ws_bytes : 0, need);
+  if (need && (uintptr_t)ws % 8) return fpi::fail(FP_EARG, "%s: misaligned workspace", fn);
+  if (T == 0) return fpi::ok();
+  const Plan p = plan_rows(dt, T, V);
+  uint64_t* keys = need ? (uint64_t*)ws : nullptr;
+  float* stats = need ? (float*)(keys + (int64_t)T * p.splits * top) : nullptr;
+  const LogArgs a{X, ldx, T, V, tokens, id_bytes == 8, 1.0f / temperature, top, p.splits, p.per, logprob, entropy, max, logsum,
+                  top_logprobs, top_ids, stats, keys};
+  if (dt == FP_F32) rc = launch_rows<float>(a, p.nv, stream);
+  else if (dt == FP_F16) rc = launch_rows<__half>(a, p.nv, stream);
+  else rc = launch_rows<__hip_bfloat16>(a, p.nv, stream);
+  return rc ? rc : fpi::ok();
+}
+
+extern "C" int fp_token_logprobs_backward(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
+                                          int32_t id_bytes, float temperature, const float* dlogprob, const float* dentropy,
+                                          const float* max, const float* logsum, const float* entropy, void* dX, int64_t lddx,
+                                          hipStream_t stream) {
+  const char* fn = "fp_token_logprobs_backward";
+  int rc = check_rows(fn, dt, X, ldx, T, V, tokens, id_bytes, temperature);
+  if (rc) return rc;
+  if (lddx < V) return fpi::fail(FP_ESHAPE, "%s: leading dimension too small", fn);
+  if (T == 0 || V == 0) return fpi::ok();
+  if (!max || !logsum || !entropy || !dX) return fpi::fail(FP_EARG, "%s: null pointer", fn);
+  if (((uintptr_t)dlogprob | (uintptr_t)dentropy | (uintptr_t)max | (uintptr_t)logsum | (uintptr_t)entropy) % 4 ||
+      (uintptr_t)dX % elem_bytes(dt))
+    return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  const LogBwdArgs a{X, ldx, T, V, tokens, id_bytes == 8, 1.0f / temperature, dlogprob, dentropy, max, logsum, entropy, dX, lddx, 0};
+  if (dt == FP_F32) launch_backward<float>(a, stream);
+  else if (dt == FP_F16) launch_backward<__half>(a, stream);
+  else launch_backward<__hip_bfloat16>(a, stream);
+  rc = fpi::check_launch("logprob_backward_kernel");
+  return rc ? rc : fpi::ok();
+}
