@@ -20,7 +20,8 @@ using sdev::load_elem;
 using sdev::v4i;
 
 constexpr int NT = 256;
-constexpr int CAP = 1024;  // candidates in LDS; also the most that the parts of a row hand over
+constexpr int CAP = 768;  // candidates of a wave in LDS: a vector of every lane finds room beside a row's top
+constexpr int PARTS = 32;  // of a row, at most
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct LogArgs {
@@ -91,32 +92,79 @@ __device__ __forceinline__ Stats block_stats(Stats v, float k2, float (*red)[3])
   return all;
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) { return fpi::shfl_xor_u64(v, m); }
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
-// The candidates of a row's part: distinct keys in LDS.
-struct Candidates {
-  uint64_t key[CAP], best[FP_MAX_TOP], group[NT / 4], tau;
-  int n;
+// A wave's keys in LDS.
+struct Keys {
+  __attribute__((aligned(16))) uint64_t at[CAP + 8], lane[64];
+  uint64_t best[FP_MAX_TOP];
 };
 
-// The k greatest of the n <= CAP keys, to the front of `key` in descending
-// order, by counting for each how many are greater. Returns how many there are.
-__device__ __forceinline__ int keep_top(Candidates& c, int n, int k) {
-  if ((int)threadIdx.x < k) c.best[threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += NT) {
-    const uint64_t mine = c.key[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += c.key[j] > mine;
-    if (rank < k) c.best[rank] = mine;
+// How many of m keys, which zeros follow to a multiple of eight, are greater.
+__device__ __forceinline__ int greater(const uint64_t* key, int m, uint64_t mine) {
+  typedef unsigned long long Two __attribute__((ext_vector_type(2)));
+  int r = 0;
+  for (int j = 0; j < m; j += 8) {
+    Two x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *(const Two*)&key[j + 2 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r += (x[i][0] > mine) + (x[i][1] > mine);
   }
-  __syncthreads();
-  const int have = min(n, k);
-  if ((int)threadIdx.x < have) c.key[threadIdx.x] = c.best[threadIdx.x];
-  if (threadIdx.x == 0) c.n = have;
-  __syncthreads();
-  return have;
+  return r;
 }
+
+// The k <= FP_MAX_TOP greatest of the keys that a wave is offered, among n
+// candidates in LDS that are cut to k where room is short. Every lane of the wave
+// takes part in every call; no two keys are equal.
+struct Top {
+  Keys* c;
+  int k, n;
+  uint64_t lim;  // lesser keys are not among them
+  float least;   // their values' bound
+  __device__ __forceinline__ Top(Keys* c_, int k_) : c(c_), k(k_), n(0), lim(0), least(-__builtin_inff()) {}
+  __device__ __forceinline__ void bound(uint64_t l) {
+    if (l <= lim) return;
+    lim = l;
+    least = key_value(l);
+  }
+  // the candidates to the k greatest in descending order, by counting for each how many are greater
+  __device__ __forceinline__ void sort() {
+    const int lane = threadIdx.x & 63;
+    if (lane < 8) c->at[n + lane] = 0;
+    wave_sync();
+    for (int i = lane; i < n; i += 64) {
+      const uint64_t mine = c->at[i];
+      const int r = greater(c->at, n, mine);
+      if (r < k) c->best[r] = mine;
+    }
+    wave_sync();
+    n = min(n, k);
+    if (lane < n) c->at[lane] = c->best[lane];
+    wave_sync();
+    if (n == k) bound(fpi::readlane_u64(c->best[k - 1], 0) + 1);
+  }
+  // room for `more` keys, at most CAP - FP_MAX_TOP
+  __device__ __forceinline__ void room(int more) {
+    if (n + more > CAP) sort();
+  }
+  __device__ __forceinline__ void offer(uint64_t key, bool in) {
+    const uint64_t who = __ballot(in && key >= lim);
+    if (who >> (threadIdx.x & 63) & 1) c->at[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0))] = key;
+    n += __popcll(who);
+  }
+  // one key a lane (0: none) of what will be offered: their k-th greatest bounds what is looked for
+  __device__ __forceinline__ void bound_by(uint64_t key) {
+    c->lane[threadIdx.x & 63] = key;
+    wave_sync();
+    const uint64_t kth = __ballot(key && greater(c->lane, 64, key) == k - 1);
+    wave_sync();
+    if (kth) bound(fpi::readlane_u64(key, __builtin_ctzll(kth)));
+  }
+};
 
 // What a row's statistics and its sorted keys say, written down.
 template <typename E>
@@ -140,30 +188,26 @@ __device__ __forceinline__ void finish_row(const LogArgs& a, int64_t t, const St
   }
 }
 
-// A workgroup to a row's part, a chunk of NV vectors a thread at a time.
+// A workgroup to a row's part, a chunk of NV vectors a thread at a time. Each wave
+// has statistics and candidates of its own, so that no wave waits for another
+// before the end of the part. The candidates' bound is first the k-th greatest of
+// the lanes' maxima, then that of the candidates.
 template <typename E, int NV>
-__global__ __launch_bounds__(NT) void logprob_kernel(LogArgs a) {
+__global__ __launch_bounds__(NT, 4) void logprob_kernel(LogArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), CH = NT * NV * EV;
-  __shared__ Candidates cand;
+  __shared__ Keys keys[NT / 64];
+  __shared__ int found[NT / 64];
   __shared__ float red[NT / 64][3];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const float k2 = a.inv_t * LOG2E;
   const int64_t tasks = (int64_t)a.T * a.splits;
   for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int64_t t = task / a.splits;
-    const int part = (int)(task % a.splits);
     const E* row = (const E*)a.X + t * a.ldx;
-    const int64_t lo = (int64_t)part * a.per * CH;
+    const int64_t lo = (task % a.splits) * a.per * CH;
     const int64_t hi = min(lo + (int64_t)a.per * CH, (int64_t)a.V);
     Stats st{-__builtin_inff(), 0.f, 0.f};
-    int n = 0;  // candidates, and whether they hold `top` sorted ones already
-    bool full = false;
-    uint64_t kth = 0;
-    if (a.top) {
-      __syncthreads();
-      if (tid == 0) cand.n = 0;
-      __syncthreads();
-    }
+    Top top(&keys[wave], a.top);
     for (int64_t base = lo; base < hi; base += CH) {
       v4i raw[NV];
       if (base + CH <= a.V) {
@@ -184,13 +228,22 @@ __global__ __launch_bounds__(NT) void logprob_kernel(LogArgs a) {
             }
         }
       }
-      float mt = -__builtin_inff();
+      // (each pass converts anew: kept, the floats of a chunk would take the registers of two workgroups)
+      auto anew = [&]() {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) asm volatile("" : "+v"(raw[v]));
+      };
+      float vm[NV], mt = -__builtin_inff();
 #pragma unroll
-        for (int e = 0; e < EV; ++e) mt = fmaxf(mt, load_elem<E>(raw[v], e));
+      for (int v = 0; v < NV; ++v) {
+        vm[v] = -__builtin_inff();
+#pragma unroll
+        for (int e = 0; e < EV; ++e) vm[v] = fmaxf(vm[v], load_elem<E>(raw[v], e));
+        mt = fmaxf(mt, vm[v]);
+      }
       if (mt > st.m) st = at_max(st, mt, k2);
       const float m0 = st.m == -__builtin_inff() ? 0.f : st.m;
+      anew();
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -200,137 +253,97 @@ __global__ __launch_bounds__(NT) void logprob_kernel(LogArgs a) {
           st.u = __builtin_fmaf(fmaxf(d, -1e30f), p, st.u);
         }
       if (!a.top) continue;
-      // ---- candidates for the top
+      const uint64_t who = __ballot(mt >= top.least);
+      if (!who) continue;
+      anew();
       auto index = [&](int v, int e) { return (uint32_t)(base + (v * NT + tid) * EV + e); };
-      // a key that at least `top` of the chunk's reach: of the maxima of 64 groups of four threads
-      auto group_key = [&]() -> uint64_t {
+      if (__popcll(who) >= a.top) {
         uint64_t best = 0;
 #pragma unroll
         for (int v = NV - 1; v >= 0; --v)
+          if (vm[v] == mt)
 #pragma unroll
-          for (int e = EV - 1; e >= 0; --e)
-            if (load_elem<E>(raw[v], e) == mt) best = make_key(mt, index(v, e));
+            for (int e = EV - 1; e >= 0; --e)
+              if (load_elem<E>(raw[v], e) == mt) best = make_key(mt, index(v, e));
+        top.bound_by(best);
+      }
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-          const uint64_t o = shfl_xor64(best, x);
-          best = o > best ? o : best;
-        }
-        if (tid == 0) cand.tau = 0;
-        if (tid % 4 == 0) cand.group[tid / 4] = best;
-        __syncthreads();
-        if (tid < 64) {
-          const uint64_t mine = cand.group[tid];
-          int rank = 0;
-#pragma unroll 8
-          for (int i = 0; i < 64; ++i) rank += cand.group[i] > mine;
-          if (rank == a.top - 1) cand.tau = mine;
-        }
-        __syncthreads();
-        return cand.tau;
-      };
-      auto gather = [&](uint64_t lim) {
-        const float least = lim ? key_value(lim) : -__builtin_inff();
-        if (mt >= least) {
+      for (int v = 0; v < NV; ++v)
+        if (__ballot(vm[v] >= top.least)) {
+          top.room(64 * EV);
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < EV; ++e) {
-              const float x = load_elem<E>(raw[v], e);
-              if (x >= least) {
-                const uint64_t k = make_key(x, index(v, e));
-                if (k >= lim) {
-                  const int at = atomicAdd(&cand.n, 1);
-                  if (at < CAP) cand.key[at] = k;
-                }
-              }
-            }
-        }
-        __syncthreads();
-        const int all = cand.n;
-        __syncthreads();  // the next candidates come after every thread has read it
-        return all;
-      };
-      uint64_t lim = full ? kth + 1 : group_key();
-      int got = gather(lim);
-      if (got > CAP) {  // uniform
-        n = keep_top(cand, n, a.top);
-        if (n == a.top) lim = max(lim, cand.key[n - 1] + 1);
-        lim = max(lim, group_key());
-        got = gather(lim);
-        if (got > CAP) {  // one at a time, from the greatest down
-          uint64_t below = ~0ull;
-          got = n;
-          for (int j = 0; j < a.top; ++j) {
-            uint64_t best = 0;
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-              for (int e = 0; e < EV; ++e) {
-                const float x = load_elem<E>(raw[v], e);
-                const uint64_t k = make_key(x, index(v, e));
-                if (x == x && k < below && k > best) best = k;
-              }
-#pragma unroll
-            for (int x = 32; x; x >>= 1) {
-              const uint64_t o = shfl_xor64(best, x);
-              best = o > best ? o : best;
-            }
-            __syncthreads();
-            if ((tid & 63) == 0) cand.group[tid >> 6] = best;
-            __syncthreads();
-            best = 0;
-            for (int w = 0; w < NT / 64; ++w) best = max(best, cand.group[w]);
-            if (best < lim || best == 0) break;  // uniform
-            if (tid == 0) cand.key[got] = best;
-            ++got;
-            below = best;
+          for (int e = 0; e < EV; ++e) {
+            const float x = load_elem<E>(raw[v], e);
+            if (__ballot(x >= top.least)) top.offer(make_key(x, index(v, e)), x >= top.least);
           }
-          __syncthreads();
-          if (tid == 0) cand.n = got;
-          __syncthreads();
         }
-      }
-      n = got;
-      if (!full || n > CAP / 2) {
-        n = keep_top(cand, n, a.top);
-        full = n == a.top;
-        if (full) kth = cand.key[n - 1];
-      }
+      if (top.n > a.top) top.sort();
     }
-    if (a.top) n = keep_top(cand, n, a.top);
+    if (a.top) {
+      top.sort();
+      if (lane == 0) found[wave] = top.n;
+    }
     st = block_stats(st, k2, red);
-    if (a.splits == 1) {
-      finish_row<E>(a, t, st, cand.key, n);
-    } else {
-      if (tid == 0) {
-        a.stats[task * 3] = st.m;
-        a.stats[task * 3 + 1] = st.s;
-        a.stats[task * 3 + 2] = st.u;
+    if (wave == 0) {
+      if (a.top) {
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w) top.offer(lane < found[w] ? keys[w].at[lane] : 0, lane < found[w]);
+        top.sort();
       }
-      if (tid < a.top) a.keys[task * a.top + tid] = tid < n ? cand.key[tid] : 0;
+      if (a.splits == 1) {
+        finish_row<E>(a, t, st, keys[0].at, top.n);
+      } else {
+        if (tid == 0) {
+          a.stats[task * 3] = st.m;
+          a.stats[task * 3 + 1] = st.s;
+          a.stats[task * 3 + 2] = st.u;
+        }
+        if (tid < a.top) a.keys[task * a.top + tid] = tid < top.n ? keys[0].at[tid] : 0;
+      }
     }
+    __syncthreads();  // the next row's candidates take the place of these
   }
 }
 
-// A row's parts joined.
+// A row's parts joined, a wave to a row. The parts' keys are sorted: the k-th
+// greatest of their first ones bounds what is looked for.
 template <typename E>
-__global__ __launch_bounds__(NT) void logprob_join_kernel(LogArgs a) {
-  __shared__ Candidates cand;
-  __shared__ float red[NT / 64][3];
-  const int tid = threadIdx.x;
+__global__ __launch_bounds__(64) void logprob_join_kernel(LogArgs a) {
+  __shared__ Keys keys;
+  const int lane = threadIdx.x;
   const float k2 = a.inv_t * LOG2E;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     Stats st{-__builtin_inff(), 0.f, 0.f};
-    if (tid < a.splits) {
-      const float* p = a.stats + (t * a.splits + tid) * 3;
+    if (lane < a.splits) {
+      const float* p = a.stats + (t * a.splits + lane) * 3;
       st = Stats{p[0], p[1], p[2]};
     }
-    int n = a.splits * a.top;  // at most CAP
-    __syncthreads();
-    for (int i = tid; i < n; i += NT) cand.key[i] = a.keys[t * n + i];
-    if (n) n = keep_top(cand, n, a.top);
-    st = block_stats(st, k2, red);
-    finish_row<E>(a, t, st, cand.key, n);
+    Top top(&keys, a.top);
+    if (a.top) {
+      const uint64_t* from = a.keys + t * a.splits * a.top;
+      const int n = a.splits * a.top;  // at most PARTS FP_MAX_TOP
+      uint64_t key[PARTS * FP_MAX_TOP / 64];
+#pragma unroll
+      for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) key[i] = lane + 64 * i < n ? from[lane + 64 * i] : 0;
+      if (a.splits >= a.top) top.bound_by(lane < a.splits ? from[lane * a.top] : 0);
+#pragma unroll
+      for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) {
+        top.room(64);
+        top.offer(key[i], key[i] != 0);
+      }
+      top.sort();
+    }
+    float m = st.m;
+#pragma unroll
+    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+    st = at_max(st, m, k2);
+#pragma unroll
+    for (int x = 32; x; x >>= 1) {
+      st.s += __shfl_xor(st.s, x, 64);
+      st.u += __shfl_xor(st.u, x, 64);
+    }
+    finish_row<E>(a, t, st, keys.at, top.n);
+    wave_sync();
   }
 }
 
@@ -408,7 +421,7 @@ Plan plan_rows(fp_dtype dt, int32_t T, int32_t V) {
   if (c == 0 || T == 0) return p;
   int64_t s = (1024 + T - 1) / T;
   s = s < c ? s : c;
-  s = s < 32 ? s : 32;
+  s = s < PARTS ? s : PARTS;
   p.per = (int)((c + s - 1) / s);
   p.splits = (int)((c + p.per - 1) / p.per);
   return p;
@@ -437,7 +450,7 @@ int launch_rows(const LogArgs& a, int nv, hipStream_t st) {
   else logprob_kernel<E, 2><<<grid, dim3(NT), 0, st>>>(a);
   int rc = fpi::check_launch("logprob_kernel");
   if (rc || a.splits == 1) return rc;
-  logprob_join_kernel<E><<<dim3((unsigned)(a.T < (1 << 20) ? a.T : 1 << 20)), dim3(NT), 0, st>>>(a);
+  logprob_join_kernel<E><<<dim3((unsigned)(a.T < (1 << 20) ? a.T : 1 << 20)), dim3(64), 0, st>>>(a);
   return fpi::check_launch("logprob_join_kernel");
 }
 
