@@ -10,12 +10,16 @@
 // scaled_dev.hpp from fp32, and y rounded once. What it must move is the weights
 // of the experts that any token meets; everything else is a few rows.
 //
-// First launch: a workgroup to 32 hidden units of an expert and all of the
-// expert's tokens; it reads the ids, finds which expert is its, quantizes the
-// tokens' rows as it multiplies, and leaves a (fp32) with each tile's largest
-// magnitude, from which the second launch has a row's scale. Second launch: a
-// workgroup to 32 outputs of an expert; the last one of these outputs to arrive
-// adds the experts' parts of every token in the order of its choices.
+// Two launches: the hidden units, then the outputs. In each, the met experts'
+// panels of 32 weight rows are numbered expert after expert, and every workgroup
+// takes an equal range of them, whatever the ids say: it reads the ids, finds its
+// experts and their tokens, quantizes the tokens' rows as it multiplies and keeps
+// its weights' loads going from panel to panel. The first launch leaves a (fp32)
+// with each panel's largest magnitude, from which the second has a row's scale;
+// in the second, the last workgroup to arrive at 32 outputs adds the experts'
+// parts of every token in the order of its choices. For more than FEW tokens,
+// whose rows an expert's workgroups would each quantize again, two launches
+// between do that once.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
@@ -25,13 +29,14 @@
 
 namespace {
 
-constexpr int NW = 8, NT = NW * 64;       // waves, each with units of K in turn
+constexpr int NW = 4, NT = NW * 64;       // waves, each with units of K in turn
 constexpr int SLOTS = FP_MAX_FEW_SLOTS;   // T K
-constexpr int ROWS = 32;                  // of an expert at a time
-constexpr int UK = 2 * WP_BK;             // bytes of K in a unit
-constexpr int XP = UK + 16;               // LDS bytes of a row's unit
+constexpr int FEW = 8;                    // tokens whose rows are quantized where they are multiplied
 constexpr int RP = 36;                    // LDS words of a row's sums
-constexpr int PF = 2;                     // units of weights in registers
+
+// Global memory, which the compiler does not see of an address that it reads from
+// memory (and then loads through the path that also serves LDS).
+typedef const __attribute__((address_space(1))) int8_t* Weights;
 
 struct Ids {
   const void* p;
@@ -46,16 +51,18 @@ struct FewArgs {
   Ids ids;
   const void* X;  // [T] tokens' rows (first launch)
   int64_t ldx;
-  const float* xs;             // of int8 X
+  const float* xs;             // of int8 rows
   const int8_t* const* W[2];   // the experts' packed weights: up and gate, or down
   const float* ws[2];          // their scales
   int64_t ldws[2];
   int32_t d_in, d_out;         // of this launch's products
   int32_t nb;                  // K blocks
-  float* A;                    // [slots][ff]
-  float* top;                  // [slots][tiles of ff]: largest magnitude
-  int32_t tiles;               // of ff
-  uint32_t* count;             // arrivals at each tile of the output
+  int32_t panels;              // of 32 outputs
+  float* A;                    // [slots][lda]: ff values, then whole pieces
+  int64_t lda;
+  float* top;                  // [slots][ldt]: largest magnitude of each panel of ff, then zeros to whole pieces
+  int32_t ldt;
+  uint32_t* count;             // arrivals at each 32 outputs
   float* part;                 // [slots][d]: D a_s
   const float* weights;        // [T][K]
   void* Y;
@@ -63,84 +70,91 @@ struct FewArgs {
   int32_t y_dt, n_count;
 };
 
+template <typename XT>
+constexpr int rows_of() { return sizeof(XT) == 1 ? 32 : 8; }  // of an expert at a time: 8 where they are quantized here
+template <typename XT>
+constexpr int wgs_of() { return sizeof(XT) == 1 ? 3 : 4; }  // workgroups that a CU holds
+constexpr int CUS = 256;
+
+// A unit of K: the blocks of it that a wave takes together, 8 KiB of weights (4
+// for 32 rows and one matrix, for the sake of LDS).
+template <int MAPS, int ROWS>
+struct Unit {
+  static constexpr int BLOCKS = ROWS == 8 ? 4 / MAPS : 2, K = BLOCKS * WP_BK, PIECES = K / 128, XP = K + 16;
+};
+
+template <int MAPS, int ROWS>
 struct Lds {
-  __attribute__((aligned(16))) int8_t x[NW * ROWS * XP];  // a wave's rows; then the waves' sums
-  uint16_t list[SLOTS];       // the expert's slots
-  uint64_t mask[SLOTS / 64];
+  __attribute__((aligned(16))) int8_t x[NW][ROWS * Unit<MAPS, ROWS>::XP];  // a wave's rows
+  __attribute__((aligned(16))) int32_t red[NW][ROWS * RP];           // the waves' sums
+  uint16_t id[SLOTS], list[SLOTS];                                   // the slots' experts (NONE: no expert); an expert's slots
+  uint16_t met[FP_MAX_EXPERTS];                                      // the experts that any slot has, ascending
   uint32_t bits[FP_MAX_EXPERTS / 32];
-  float part[ROWS][NW];
-  sdev::RowScale rs[ROWS];
-  uint32_t last;
+  float part[8][NW];
+  sdev::RowScale rs[8];
+  int n, last;
+  uint16_t tile[NT];
 };
-static_assert(NW * ROWS * XP >= NW * ROWS * RP * 4, "the sums fit the rows' space");
-static_assert(SLOTS <= 2 * NT && SLOTS <= 65536, "two slots a thread");
+constexpr int NONE = 0xFFFF;
+static_assert(FP_MAX_EXPERTS < NONE && SLOTS <= NONE, "experts and slots in 16 bits");
 
-struct Expert {
-  int e, n, present;  // -1: there are not so many
-};
-
-// The j-th expert that any slot has, its slots (ascending, in lds.list), and how
-// many experts there are.
-__device__ __forceinline__ Expert find_expert(const Ids& ids, int j, Lds& lds) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, N = ids.T * ids.K;
-  int id[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) id[i] = tid + i * NT < N ? ids.at(tid + i * NT) : -1;
-  if (tid < FP_MAX_EXPERTS / 32) lds.bits[tid] = 0;
+// The slots' experts and the list of those met. Returns how many are met.
+template <typename L>
+__device__ __forceinline__ int find_experts(const Ids& ids, L& lds) {
+  const int tid = threadIdx.x, N = ids.T * ids.K, words = (ids.E + 31) / 32;
+  for (int i = tid; i < words; i += NT) lds.bits[i] = 0;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (id[i] >= 0) atomicOr(&lds.bits[id[i] >> 5], 1u << (id[i] & 31));
-  __syncthreads();
-  const uint32_t word = lane < FP_MAX_EXPERTS / 32 ? lds.bits[lane] : 0;
-  const int mine = __popc(word);
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
-  }
-  const int present = __builtin_amdgcn_readlane(incl, 31);
-  if (j >= present) return Expert{-1, 0, present};  // uniform
-  const uint64_t has = __ballot(lane < 32 && incl - mine <= j && j < incl);
-  const int src = __builtin_ctzll(has);
-  uint32_t left = __builtin_amdgcn_readlane((int)word, src);
-  for (int skip = j - (__builtin_amdgcn_readlane(incl, src) - __popc(left)); skip > 0; --skip) left &= left - 1;
-  const int e = src * 32 + __builtin_ctz(left);
-  uint64_t m[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    m[i] = __ballot(id[i] == e);
-    if (lane == 0 && i * NW + wave < SLOTS / 64) lds.mask[i * NW + wave] = m[i];
+  for (int i = tid; i < N; i += NT) {
+    const int e = ids.at(i);
+    lds.id[i] = (uint16_t)e;  // NONE for -1
+    if (e >= 0) atomicOr(&lds.bits[e >> 5], 1u << (e & 31));
   }
   __syncthreads();
-  int n = 0, before[2] = {0, 0};
-#pragma unroll
-  for (int c = 0; c < SLOTS / 64; ++c) {
-    const int k = __popcll(lds.mask[c]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (c < i * NW + wave) before[i] += k;
-    n += k;
+  int present = 0;
+  for (int e = tid; e - tid < ids.E; e += NT) {
+    int rank = 0, all = 0;
+    for (int w = 0; w < words; ++w) {
+      const int c = __popc(lds.bits[w]);
+      rank += w < e >> 5 ? c : 0;
+      all += c;
+    }
+    present = all;
+    if (e < ids.E && (lds.bits[e >> 5] >> (e & 31) & 1)) lds.met[rank + __popc(lds.bits[e >> 5] & ((1u << (e & 31)) - 1))] = (uint16_t)e;
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (id[i] == e) lds.list[before[i] + __popcll(m[i] & ((1ull << lane) - 1))] = (uint16_t)(tid + i * NT);
   __syncthreads();
-  return Expert{e, n, present};
+  return __builtin_amdgcn_readfirstlane(present);
 }
 
-// The largest magnitudes of nr rows of d values (infinite with an infinity or a
-// NaN) as scales in lds.rs; the entries past nr quantize to zeros. Few rows are
-// cut over the waves.
-template <typename F>
-__device__ __forceinline__ void row_scales(int nr, int64_t d, const F* (*row)(const FewArgs&, int), const FewArgs& a, int r0,
-                                           Lds& lds) {
+// The slots of expert e, ascending, in lds.list. Returns how many.
+template <typename L>
+__device__ __forceinline__ int find_slots(const Ids& ids, int e, L& lds) {
+  const int N = ids.T * ids.K, lane = threadIdx.x & 63;
+  __syncthreads();  // the last expert's list is read
+  if (threadIdx.x < 64) {
+    int n = 0;
+    for (int i = lane; i - lane < N; i += 64) {
+      const bool has = i < N && lds.id[i] == e;
+      const uint64_t who = __ballot(has);
+      if (has) lds.list[n + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)i;
+      n += (int)__popcll(who);
+    }
+    if (lane == 0) lds.n = n;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(lds.n);
+}
+
+// The largest magnitudes of nr <= 8 rows of d values (infinite with an infinity
+// or a NaN) as scales in lds.rs; the entries past nr quantize to zeros. Few rows
+// are cut over the waves.
+template <typename F, bool WHOLE, typename Row, typename L>
+__device__ __forceinline__ void row_scales(int nr, int64_t d, Row row, L& lds) {
   constexpr int EV = 16 / (int)sizeof(F);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cut = nr <= 1 ? 8 : (nr <= 2 ? 4 : (nr <= 4 ? 2 : 1)), part = wave % cut;
+  const int cut = nr <= 1 ? 4 : (nr <= 2 ? 2 : 1), part = wave % cut;
+  __syncthreads();  // the last rows' scales are read
   for (int r = wave / cut; r < nr; r += NW / cut) {
-    const F* p = row(a, lds.list[r0 + r]);
+    const F* p = row(r);
     float top = 0.f;
     bool bad = false;
     for (int64_t k0 = (int64_t)(part * 64 + lane) * EV; k0 < d; k0 += (int64_t)cut * 64 * EV * 4) {
@@ -149,7 +163,10 @@ __device__ __forceinline__ void row_scales(int nr, int64_t d, const F* (*row)(co
       for (int i = 0; i < 4; ++i) {
         const int64_t k = k0 + (int64_t)i * cut * 64 * EV;
         raw[i] = sdev::v4i{0, 0, 0, 0};
-        if (k < d) raw[i] = sdev::load16u(p + k, d - k);
+        if (k < d) {
+          if constexpr (WHOLE) raw[i] = *(const typename sdev::AnyVec<sizeof(F)>::type*)(p + k);
+          else raw[i] = sdev::load16u(p + k, d - k);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -166,7 +183,7 @@ __device__ __forceinline__ void row_scales(int nr, int64_t d, const F* (*row)(co
     if (lane == 0) lds.part[r][part] = top;
   }
   __syncthreads();
-  if (threadIdx.x < ROWS) {
+  if (threadIdx.x < 8) {
     sdev::RowScale rs{0.f, 0.f, 0.f};
     if ((int)threadIdx.x < nr) {
       float top = 0.f;
@@ -177,17 +194,41 @@ __device__ __forceinline__ void row_scales(int nr, int64_t d, const F* (*row)(co
   }
   __syncthreads();
 }
+static_assert(NW == 4, "row_scales cuts a row over four waves at most");
+
+// sdev::quantize of four values, as the bytes of a word. 1.5 2^23 added to a value
+// of at most 127 rounds it to the nearest, ties to even, and leaves it in the low
+// bits (the maximum's own product rounds to 127 at most); a bad row's values
+// become zeros. Five instructions a value instead of twelve: it is every
+// workgroup of an expert that quantizes the expert's rows.
+__device__ __forceinline__ uint32_t quantize4(const float (&x)[4], const sdev::RowScale& rs) {
+#pragma clang fp contract(off)
+  uint32_t b[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float p = (x[q] * rs.pre) * rs.inv;
+    b[q] = __float_as_uint(p + 12582912.0f);
+  }
+  const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+  return rs.pre == 0.f ? 0u : lo | hi;
+}
 
 // 16 values of a row from column k on, as int8.
-template <typename XT>
+// WHOLE: rows are read in whole pieces (d is a multiple of 16, or what follows d
+// in the row may be read: it meets zero weights).
+template <typename XT, bool WHOLE>
 struct Piece {
   static constexpr int EV = 16 / (int)sizeof(XT), N = 16 / EV;
   sdev::v4i raw[N];
   __device__ __forceinline__ void load(const XT* p, int k, int d) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      raw[i] = sdev::v4i{0, 0, 0, 0};
-      if (k + i * EV < d) raw[i] = sdev::load16u(p + k + i * EV, d - k - i * EV);
+      if constexpr (WHOLE) {
+        raw[i] = *(const typename sdev::AnyVec<sizeof(XT)>::type*)(p + (k < d ? k : 0) + i * EV);
+      } else {
+        raw[i] = sdev::v4i{0, 0, 0, 0};
+        if (k + i * EV < d) raw[i] = sdev::load16u(p + k + i * EV, d - k - i * EV);
+      }
     }
   }
   __device__ __forceinline__ v4i bytes(const sdev::RowScale& rs) const {
@@ -197,162 +238,163 @@ struct Piece {
       v4i b;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t x = 0;
+        float x[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int e = 4 * w + q;
-          x |= (uint32_t)(sdev::quantize(sdev::load_elem<XT>(raw[e / EV], e % EV), rs) & 255) << (8 * q);
-        }
-        b[w] = (int)x;
+        for (int q = 0; q < 4; ++q) x[q] = sdev::load_elem<XT>(raw[(4 * w + q) / EV], (4 * w + q) % EV);
+        b[w] = (int)quantize4(x, rs);
       }
       return b;
     }
   }
 };
 
-// Z of rows r0.. r0 + nr - 1 of the list (at most 8 XR) and the 32 outputs of
-// tile `tile`, for MAPS matrices: z[map][m] of thread tid is row tid / 32 + 16 m,
-// output tid % 32. Wave w takes units w, w + NW, ... of K.
-template <int XR, int MAPS, typename XT>
-__device__ __forceinline__ void products(const FewArgs& a, const int8_t* const (&W)[MAPS], int tile, int r0, int nr,
-                                         const XT* (*row)(const FewArgs&, int), Lds& lds, int32_t (&z)[MAPS][2]) {
-  constexpr int PX = XR == 1 ? 1 : 0;  // a unit of X ahead where it is small
+// The products of nr rows (at most ROWS; row(i) their addresses) with the panels
+// [t0, t1) of MAPS matrices: for each panel done(panel, z), where z[map][m] of
+// thread tid is the integer product of row tid / 32 + (NT / 32) m and the panel's
+// output tid % 32. Wave w takes units w, w + NW, ... of K. Loads return in the
+// order in which they were issued: a unit's rows go before its weights, and both
+// as soon as the unit before them is multiplied, over the panels' ends.
+template <int MAPS, typename XT, bool WHOLE, typename Row, typename L, typename Done>
+__device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MAPS], int t0, int t1, int nr, Row row, L& lds,
+                                         Done done) {
+  constexpr int ROWS = rows_of<XT>();
+  using U = Unit<MAPS, ROWS>;
+  constexpr int XR = ROWS / 8, ZR = (ROWS + NT / 32 - 1) / (NT / 32);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int NB = a.nb, NU = (NB + 1) / 2;
-  const int8_t* pw[MAPS];
-#pragma unroll
-  for (int i = 0; i < MAPS; ++i) pw[i] = W[i] + (int64_t)tile * NB * (WP_BK * 32);
-  v4i wf[PF][MAPS][4];
-  auto wload = [&](int slot, int u) {
-#pragma unroll
-    for (int i = 0; i < MAPS; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        wf[slot][i][q] = *(const v4i*)(pw[i] + (int64_t)min(2 * u + q / 2, NB - 1) * (WP_BK * 32) + 1024 * (q % 2) + lane * 16);
-  };
-  const int kc = (lane & 7) * 16;
+  const int NB = a.nb, NU = (NB + U::BLOCKS - 1) / U::BLOCKS;
+  v4i wf[MAPS][U::BLOCKS][2];
+  Piece<XT, WHOLE> x[XR][U::PIECES];
   const XT* px[XR];
-  sdev::RowScale rs[XR];
 #pragma unroll
   for (int c = 0; c < XR; ++c) {
     const int rr = 8 * c + (lane >> 3);
-    px[c] = row(a, lds.list[r0 + (rr < nr ? rr : 0)]);
-    if constexpr (sizeof(XT) > 1) rs[c] = lds.rs[rr];
+    px[c] = row(rr < nr ? rr : 0);
   }
-  int8_t* xw = lds.x + wave * (ROWS * XP);
-  int8_t* xs = xw + (lane >> 3) * XP + kc;  // stores: row lane / 8 of 8, piece lane % 8
-  const int8_t* xf = xw + r * XP + 32 * h;  // fragments
-  v16i acc[MAPS];
+  const int kc = (lane & 7) * 16;  // a load of rows: lane / 8 of eight, piece lane % 8
+  auto load = [&](int t, int u) {
 #pragma unroll
-  for (int i = 0; i < MAPS; ++i)
+    for (int c = 0; c < XR; ++c)
+      if (c == 0 || 8 * c < nr)  // uniform
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[i][v] = 0;
-  Piece<XT> x[XR];
-  if (wave < NU) {
-    const int last = wave + (NU - 1 - wave) / NW * NW;  // this wave's last unit
+        for (int g = 0; g < U::PIECES; ++g) x[c][g].load(px[c], u * U::K + 128 * g + kc, a.d_in);
 #pragma unroll
-    for (int p = 0; p < PF; ++p) wload(p, min(wave + p * NW, last));
-    if constexpr (PX) x[0].load(px[0], wave * UK + kc, a.d_in);
-    for (int u0 = wave; u0 <= last; u0 += PF * NW) {
+    for (int i = 0; i < MAPS; ++i) {
+      const Weights pw = W[i] + (int64_t)t * NB * (WP_BK * 32);
 #pragma unroll
-      for (int p = 0; p < PF; ++p) {
-        const int u = u0 + p * NW;
-        if (u <= last) {  // uniform
-          if constexpr (!PX) {
+      for (int b = 0; b < U::BLOCKS; ++b)
 #pragma unroll
-            for (int c = 0; c < XR; ++c) x[c].load(px[c], u * UK + kc, a.d_in);
-          }
+        for (int q = 0; q < 2; ++q)
+          wf[i][b][q] = *(const __attribute__((address_space(1))) v4i*)(pw + (int64_t)min(U::BLOCKS * u + b, NB - 1) * (WP_BK * 32) + 1024 * q + lane * 16);
+    }
+  };
+  sdev::RowScale rs{};
+  if constexpr (sizeof(XT) > 1) rs = lds.rs[lane >> 3];
+  int8_t* xs = lds.x[wave] + (lane >> 3) * U::XP + kc;
+  const int8_t* xf = lds.x[wave] + (r & (ROWS - 1)) * U::XP + 32 * h;  // fragments
+  if (wave < NU) load(t0, wave);
+  for (int t = t0; t < t1; ++t) {
+    v16i acc[MAPS];
 #pragma unroll
-          for (int c = 0; c < XR; ++c) *(v4i*)(xs + 8 * c * XP) = x[c].bytes(rs[c]);
-          if constexpr (PX) x[0].load(px[0], min(u + NW, last) * UK + kc, a.d_in);
-          const bool two = 2 * u + 1 < NB;
+    for (int i = 0; i < MAPS; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q >= 2 && !two) break;
-            const v4i f = *(const v4i*)(xf + WP_BK * (q / 2) + 16 * (q % 2));
+      for (int v = 0; v < 16; ++v) acc[i][v] = 0;
+    for (int u = wave; u < NU; u += NW) {
 #pragma unroll
-            for (int i = 0; i < MAPS; ++i) acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[p][i][q], f, acc[i], 0, 0, 0);
-          }
-          wload(p, min(u + PF * NW, last));
+      for (int c = 0; c < XR; ++c)
+        if (c == 0 || 8 * c < nr)
+#pragma unroll
+          for (int g = 0; g < U::PIECES; ++g) *(v4i*)(xs + 8 * c * U::XP + 128 * g) = x[c][g].bytes(rs);
+#pragma unroll
+      for (int b = 0; b < U::BLOCKS; ++b) {
+        if (b > 0 && U::BLOCKS * u + b >= NB) break;  // uniform
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const v4i f = *(const v4i*)(xf + WP_BK * b + 16 * q);
+#pragma unroll
+          for (int i = 0; i < MAPS; ++i) acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i][b][q], f, acc[i], 0, 0, 0);
         }
       }
+      const bool more = u + NW < NU;
+      if (more || t + 1 < t1) load(more ? t : t + 1, more ? u + NW : wave);
     }
+    // lane (row r, h) register 4 g + e: output 8 g + 4 h + e
+    int32_t z[MAPS][ZR];
+#pragma unroll
+    for (int i = 0; i < MAPS; ++i) {
+      __syncthreads();  // the sums before these are read
+      if (r < nr) {
+        int32_t* dst = lds.red[wave] + r * RP + 4 * h;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(v4i*)(dst + 8 * g) = v4i{acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]};
+      }
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < ZR; ++m) {
+        const int tl = tid / 32 + NT / 32 * m;
+        z[i][m] = 0;
+        if (tl < nr)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) z[i][m] += lds.red[w][tl * RP + tid % 32];
+      }
+    }
+    done(t, z);
   }
-  // lane (row r, h) register 4 g + e: output 8 g + 4 h + e
-  int32_t* red = reinterpret_cast<int32_t*>(lds.x);
-#pragma unroll
-  for (int i = 0; i < MAPS; ++i) {
-    __syncthreads();  // every wave is done with X, or with the other map's sums
-    if (r < nr) {
-      int32_t* dst = red + (wave * ROWS + r) * RP + 4 * h;
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *(v4i*)(dst + 8 * g) = v4i{acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]};
-    }
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int tl = tid / 32 + 16 * m;
-      z[i][m] = 0;
-      if (tl < nr)
-#pragma unroll
-        for (int w = 0; w < NW; ++w) z[i][m] += red[(w * ROWS + tl) * RP + tid % 32];
-    }
-  }
-  __syncthreads();
 }
 
-template <typename XT>
-__device__ const XT* token_row(const FewArgs& a, int slot) {
-  return (const XT*)a.X + (int64_t)(slot / a.ids.K) * a.ldx;
-}
-__device__ const float* hidden_row(const FewArgs& a, int slot) { return a.A + (int64_t)slot * a.d_in; }
-__device__ const float* hidden_tops(const FewArgs& a, int slot) { return a.top + (int64_t)slot * a.tiles; }
+// Where workgroup b's panels begin among all of them.
+__device__ __forceinline__ int64_t share(int64_t all, int b) { return all * b / gridDim.x; }
 
-// Hidden units [32 blockIdx.x, + 32) of the blockIdx.y-th expert that is met.
-template <int MAPS, typename XT>
-__global__ __launch_bounds__(NT) void moe_hidden_kernel(FewArgs a) {
-  __shared__ Lds lds;
+template <int MAPS, typename XT, bool WHOLE>
+__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_hidden_kernel(FewArgs a) {
+  constexpr int ROWS = rows_of<XT>();
+  __shared__ Lds<MAPS, ROWS> lds;
   const int tid = threadIdx.x;
-  if (blockIdx.x == 0 && blockIdx.y == 0)
+  if (blockIdx.x == 0)
     for (int i = tid; i < a.n_count; i += NT) a.count[i] = 0;
-  const Expert ex = find_expert(a.ids, blockIdx.y, lds);
-  if (ex.e < 0) return;
-  const int o = blockIdx.x * 32 + tid % 32;
-  const int8_t* W[MAPS];
-  float ws[MAPS];
+  const int64_t all = (int64_t)find_experts(a.ids, lds) * a.panels, end = share(all, blockIdx.x + 1);
+  for (int64_t at = share(all, blockIdx.x); at < end;) {
+    const int j = (int)(at / a.panels), t0 = (int)(at - (int64_t)j * a.panels);
+    const int t1 = (int)min((int64_t)a.panels, t0 + end - at);
+    at += t1 - t0;
+    const int e = __builtin_amdgcn_readfirstlane(lds.met[j]), n = find_slots(a.ids, e, lds);
+    Weights W[MAPS];
 #pragma unroll
-  for (int i = 0; i < MAPS; ++i) {
-    W[i] = a.W[i][ex.e];
-    ws[i] = o < a.d_out ? a.ws[i][ex.e * a.ldws[i] + o] : 0.f;
-  }
-  for (int r0 = 0; r0 < ex.n; r0 += ROWS) {
-    const int nr = min(ex.n - r0, ROWS);
-    if constexpr (sizeof(XT) > 1) row_scales<XT>(nr, a.d_in, token_row<XT>, a, r0, lds);
-    int32_t z[MAPS][2];
-    if (nr <= 8) products<1, MAPS, XT>(a, W, blockIdx.x, r0, nr, token_row<XT>, lds, z);
-    else products<4, MAPS, XT>(a, W, blockIdx.x, r0, nr, token_row<XT>, lds, z);
+    for (int i = 0; i < MAPS; ++i) W[i] = (Weights)a.W[i][e];
+    for (int r0 = 0; r0 < n; r0 += ROWS) {
+      const int nr = min(n - r0, ROWS);
+      auto row = [&](int r) { return (const XT*)a.X + (int64_t)((uint32_t)lds.list[r0 + r] / (uint32_t)a.ids.K) * a.ldx; };
+      if constexpr (sizeof(XT) > 1) row_scales<XT, WHOLE>(nr, a.d_in, row, lds);
+      products<MAPS, XT, WHOLE>(a, W, t0, t1, nr, row, lds, [&](int t, const auto& z) {
+        const int o = t * 32 + tid % 32;
+        float ws[MAPS];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int tl = tid / 32 + 16 * m;
-      if (tl >= nr) continue;
-      const int slot = lds.list[r0 + tl];
-      float xs;
-      if constexpr (sizeof(XT) > 1) xs = lds.rs[tl].scale;
-      else xs = a.xs[slot / a.ids.K];
-      float v = (float)z[MAPS - 1][m] * xs * ws[MAPS - 1];
-      v = v / (1.0f + expf(-v));
-      if constexpr (MAPS == 2) v *= (float)z[0][m] * xs * ws[0];
-      float top = fabsf(v);
-      if (!(top < __builtin_inff())) top = __builtin_inff();
-      if (o >= a.d_out) top = 0.f;
-      else a.A[(int64_t)slot * a.d_out + o] = v;
+        for (int i = 0; i < MAPS; ++i) ws[i] = tid / 32 < nr && o < a.d_out ? a.ws[i][e * a.ldws[i] + o] : 0.f;
 #pragma unroll
-      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
-      if (tid % 32 == 0) a.top[(int64_t)slot * a.tiles + blockIdx.x] = top;
+        for (int m = 0; m < (int)(sizeof(z[0]) / 4); ++m) {
+          const int tl = tid / 32 + NT / 32 * m;
+          if (tl >= nr) continue;
+          const int slot = lds.list[r0 + tl];
+          float xs;
+          if constexpr (sizeof(XT) > 1) xs = lds.rs[tl].scale;
+          else xs = a.xs[(uint32_t)slot / (uint32_t)a.ids.K];
+          float v = (float)z[MAPS - 1][m] * xs * ws[MAPS - 1];
+          v = v / (1.0f + expf(-v));
+          if constexpr (MAPS == 2) v *= (float)z[0][m] * xs * ws[0];
+          if (o < a.d_out) a.A[slot * a.lda + o] = v;
+          if (a.top) {
+            float top = fabsf(v);
+            if (!(top < __builtin_inff())) top = __builtin_inff();
+            if (o >= a.d_out) top = 0.f;
+#pragma unroll
+            for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+            if (tid % 32 == 0) a.top[(int64_t)slot * a.ldt + t] = top;
+            if (t == a.panels - 1 && tid % 32 < a.ldt - a.panels) a.top[(int64_t)slot * a.ldt + a.panels + tid % 32] = 0.f;
+          }
+        }
+      });
     }
-    __syncthreads();  // the scales are read
   }
 }
 
@@ -362,64 +404,107 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int o, float 
   else ((uint16_t*)a.Y)[at] = (uint16_t)(a.y_dt == FP_F16 ? sdev::Out<__half>::bits(f) : sdev::Out<__hip_bfloat16>::bits(f));
 }
 
-// Outputs [32 blockIdx.x, + 32) of the blockIdx.y-th expert that is met; the
-// last expert's workgroup to arrive has every token's.
-__global__ __launch_bounds__(NT) void moe_output_kernel(FewArgs a) {
-  __shared__ Lds lds;
-  const int tid = threadIdx.x, o = blockIdx.x * 32 + tid % 32;
-  const Expert ex = find_expert(a.ids, blockIdx.y, lds);
-  if (ex.e < 0) {
-    if (ex.present == 0 && blockIdx.y == 0)  // no token has an expert
-      for (int t = tid / 32; t < a.ids.T && o < a.d_out; t += NT / 32) store_out(a, t, o, 0.f);
+// Rows of XT = float are A's own, with scales from a.top, int8 ones those in X
+// with a.xs.
+template <typename XT>
+__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a) {
+  constexpr int ROWS = rows_of<XT>();
+  __shared__ Lds<1, ROWS> lds;
+  const int tid = threadIdx.x;
+  const int present = find_experts(a.ids, lds);
+  if (present == 0) {  // no token has an expert
+    for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < (int64_t)a.ids.T * a.d_out; i += (int64_t)gridDim.x * NT)
+      store_out(a, (int)(i / a.d_out), (int)(i % a.d_out), 0.f);
     return;
   }
-  const int8_t* const W[1] = {a.W[0][ex.e]};
-  const float ws = o < a.d_out ? a.ws[0][ex.e * a.ldws[0] + o] : 0.f;
-  for (int r0 = 0; r0 < ex.n; r0 += ROWS) {
-    const int nr = min(ex.n - r0, ROWS);
-    row_scales<float>(nr, a.tiles, hidden_tops, a, r0, lds);
-    int32_t z[1][2];
-    if (nr <= 8) products<1, 1, float>(a, W, blockIdx.x, r0, nr, hidden_row, lds, z);
-    else products<4, 1, float>(a, W, blockIdx.x, r0, nr, hidden_row, lds, z);
+  const int64_t all = (int64_t)present * a.panels, first = share(all, blockIdx.x), end = share(all, blockIdx.x + 1);
+  if (first == end) return;
+  for (int64_t at = first; at < end;) {
+    const int j = (int)(at / a.panels), t0 = (int)(at - (int64_t)j * a.panels);
+    const int t1 = (int)min((int64_t)a.panels, t0 + end - at);
+    at += t1 - t0;
+    const int e = __builtin_amdgcn_readfirstlane(lds.met[j]), n = find_slots(a.ids, e, lds);
+    const Weights W[1] = {(Weights)a.W[0][e]};
+    for (int r0 = 0; r0 < n; r0 += ROWS) {
+      const int nr = min(n - r0, ROWS);
+      auto row = [&](int r) { return (const XT*)a.X + (int64_t)lds.list[r0 + r] * a.ldx; };
+      if constexpr (sizeof(XT) > 1)
+        row_scales<float, true>(nr, a.ldt, [&](int r) { return a.top + (int64_t)lds.list[r0 + r] * a.ldt; }, lds);
+      products<1, XT, true>(a, W, t0, t1, nr, row, lds, [&](int t, const auto& z) {
+        const int o = t * 32 + tid % 32;
+        const float ws = tid / 32 < nr && o < a.d_out ? a.ws[0][e * a.ldws[0] + o] : 0.f;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int tl = tid / 32 + 16 * m;
-      if (tl < nr && o < a.d_out)
-        __hip_atomic_store(&a.part[(int64_t)lds.list[r0 + tl] * a.d_out + o], (float)z[0][m] * lds.rs[tl].scale * ws,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int m = 0; m < (int)(sizeof(z[0]) / 4); ++m) {
+          const int tl = tid / 32 + NT / 32 * m;
+          if (tl >= nr || o >= a.d_out) continue;
+          const int slot = lds.list[r0 + tl];
+          float xs;
+          if constexpr (sizeof(XT) > 1) xs = lds.rs[tl].scale;
+          else xs = a.xs[slot];
+          __hip_atomic_store(&a.part[(int64_t)slot * a.d_out + o], (float)z[0][m] * xs * ws, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      });
     }
-    __syncthreads();  // the scales are read
   }
-  // each thread's stores are at the agent's level before its workgroup's arrival counts
+  // each thread's stores are at the agent's level before its workgroup's arrivals count
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  if (tid == 0)
-    lds.last = __hip_atomic_fetch_add(&a.count[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)ex.present;
-  __syncthreads();
-  if (!lds.last || o >= a.d_out) return;
-  for (int t = tid / 32; t < a.ids.T; t += NT / 32) {
-    float y = 0.f;
-    for (int k = 0; k < a.ids.K; ++k) {
-      const int s = t * a.ids.K + k;
-      if (a.ids.at(s) >= 0)
-        y = __builtin_fmaf(a.weights[s], __hip_atomic_load(&a.part[(int64_t)s * a.d_out + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), y);
+  for (int64_t base = first; base < end; base += NT) {
+    __syncthreads();
+    if (tid == 0) lds.last = 0;
+    __syncthreads();
+    if (base + tid < end) {
+      const int t = (int)((base + tid) % a.panels);
+      if (__hip_atomic_fetch_add(&a.count[t], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)present)
+        lds.tile[atomicAdd(&lds.last, 1)] = (uint16_t)t;
     }
-    store_out(a, t, o, y);
+    __syncthreads();
+    const int outs = lds.last * 32;  // of each token
+    for (int i = tid; i < outs * a.ids.T; i += NT) {
+      const int t = i / outs, o = lds.tile[i % outs / 32] * 32 + i % 32;
+      if (o >= a.d_out) continue;
+      constexpr int KG = 8;  // choices whose loads are under way together
+      float y = 0.f;
+      for (int k0 = 0; k0 < a.ids.K; k0 += KG) {
+        float w[KG], v[KG];
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const int s = t * a.ids.K + min(k0 + k, a.ids.K - 1);
+          w[k] = a.weights[s];
+          // (a slot without an expert has an element here too, which nothing wrote)
+          v[k] = __hip_atomic_load(&a.part[(int64_t)s * a.d_out + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int k = 0; k < KG; ++k)
+          if (k0 + k < a.ids.K && lds.id[t * a.ids.K + k0 + k] != NONE) y = __builtin_fmaf(w[k], v[k], y);
+      }
+      store_out(a, t, o, y);
+    }
   }
 }
 
 int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
 
 struct Scratch {
-  size_t top, A, part, bytes;
+  size_t top, A, part, xs, xq, as, aq, bytes;  // xs.. aq: int8 rows, with more than FEW tokens
 };
-Scratch scratch(int64_t N, int64_t d, int64_t ff) {
-  Scratch s;
-  s.top = fpi::align_up((size_t)(d + 31) / 32 * 4, 256);
-  s.A = s.top + fpi::align_up((size_t)(N * ((ff + 31) / 32)) * 4, 256);
-  s.part = s.A + fpi::align_up((size_t)(N * ff) * 4, 256);
-  s.bytes = s.part + fpi::align_up((size_t)(N * d) * 4, 256);
+int64_t chunked(int64_t n) { return (n + 15) / 16 * 16; }
+Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
+  Scratch s{};
+  size_t at = 0;
+  auto take = [&](int64_t bytes) { const size_t p = at; at += fpi::align_up((size_t)bytes, 256); return p; };
+  take((d + 31) / 32 * 4);  // arrivals
+  s.A = take(N * chunked(ff) * 4);
+  s.part = take(N * d * 4);
+  if (T <= FEW) {
+    s.top = take(N * ((ff + 127) / 128 * 4) * 4);
+  } else {
+    s.xs = take(T * 4);
+    s.xq = take(T * chunked(d));
+    s.as = take(N * 4);
+    s.aq = take(N * chunked(ff));
+  }
+  s.bytes = at;
   return s;
 }
 
@@ -431,19 +516,24 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t d, int32_t ff) {
   return FP_OK;
 }
 
+template <int MAPS, typename XT>
+void launch_hidden_rows(const FewArgs& a, dim3 grid, hipStream_t st) {
+  if (a.d_in % 16 == 0) moe_hidden_kernel<MAPS, XT, true><<<grid, dim3(NT), 0, st>>>(a);
+  else moe_hidden_kernel<MAPS, XT, false><<<grid, dim3(NT), 0, st>>>(a);
+}
 template <int MAPS>
 void launch_hidden(int x_dt, const FewArgs& a, dim3 grid, hipStream_t st) {
-  if (x_dt == FP_I8) moe_hidden_kernel<MAPS, int8_t><<<grid, dim3(NT), 0, st>>>(a);
-  else if (x_dt == FP_F32) moe_hidden_kernel<MAPS, float><<<grid, dim3(NT), 0, st>>>(a);
-  else if (x_dt == FP_F16) moe_hidden_kernel<MAPS, __half><<<grid, dim3(NT), 0, st>>>(a);
-  else moe_hidden_kernel<MAPS, __hip_bfloat16><<<grid, dim3(NT), 0, st>>>(a);
+  if (x_dt == FP_I8) launch_hidden_rows<MAPS, int8_t>(a, grid, st);
+  else if (x_dt == FP_F32) launch_hidden_rows<MAPS, float>(a, grid, st);
+  else if (x_dt == FP_F16) launch_hidden_rows<MAPS, __half>(a, grid, st);
+  else launch_hidden_rows<MAPS, __hip_bfloat16>(a, grid, st);
 }
 
 }  // namespace
 
 extern "C" size_t fp_moe_layer_workspace(int32_t T, int32_t K, int32_t d, int32_t ff) {
   if (T < 0 || K < 1 || d < 1 || ff < 1 || (int64_t)T * K > FP_MAX_FEW_SLOTS) return 0;
-  return scratch((int64_t)T * K, d, ff).bytes;
+  return scratch(T, (int64_t)T * K, d, ff).bytes;
 }
 
 extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const float* x_scale, const void* ids, int32_t id_bytes,
@@ -468,27 +558,37 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
       ((uintptr_t)x_scale | (uintptr_t)weights | (uintptr_t)gate_scale | (uintptr_t)up_scale | (uintptr_t)down_scale) % 4 ||
       ((uintptr_t)gate | (uintptr_t)up | (uintptr_t)down) % 8)
     return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
-  const Scratch s = scratch((int64_t)T * K, d, ff);
+  const Scratch s = scratch(T, (int64_t)T * K, d, ff);
   if (!ws || ws_bytes < s.bytes) return fpi::fail(FP_EWORKSPACE, "%s: workspace %zu < %zu", fn, ws ? ws_bytes : 0, s.bytes);
   if ((uintptr_t)ws % 256) return fpi::fail(FP_EARG, "%s: workspace not 256-byte aligned", fn);
   char* const w = (char*)ws;
-  FewArgs a{};
-  a.ids = Ids{ids, id_bytes == 8, T, K, E};
-  a.X = X;
-  a.ldx = ldx;
-  a.xs = x_scale;
-  a.count = (uint32_t*)w;
-  a.top = (float*)(w + s.top);
-  a.A = (float*)(w + s.A);
-  a.part = (float*)(w + s.part);
-  a.weights = weights;
-  a.Y = Y;
-  a.ldy = ldy;
-  a.y_dt = y_dt;
-  a.tiles = (ff + 31) / 32;
-  a.n_count = (d + 31) / 32;
-  const unsigned groups = (unsigned)(T * K < E ? T * K : E);
-  FewArgs h = a;
+  const bool few = T <= FEW;
+  if (!few && x_dt != FP_I8) {
+    const int r = fp_quantize_rows(x_dt, X, ldx, T, d, (int8_t*)(w + s.xq), chunked(d), (float*)(w + s.xs), stream);
+    if (r) return r;
+    x_dt = FP_I8;
+    X = w + s.xq;
+    ldx = chunked(d);
+    x_scale = (const float*)(w + s.xs);
+  }
+  const int64_t most = T * K < E ? T * K : E;  // experts that the tokens can meet
+  auto grid = [&](int64_t panels) {  // as many workgroups as the GPU holds at once
+    const int64_t held = CUS * (x_dt == FP_I8 ? wgs_of<int8_t>() : wgs_of<float>());
+    return dim3((unsigned)(most * panels < held ? most * panels : held));
+  };
+  FewArgs h{};
+  h.ids = Ids{ids, id_bytes == 8, T, K, E};
+  h.count = (uint32_t*)w;
+  h.n_count = (d + 31) / 32;
+  h.A = (float*)(w + s.A);
+  h.lda = chunked(ff);
+  h.top = few ? (float*)(w + s.top) : nullptr;
+  h.panels = (ff + 31) / 32;
+  h.ldt = (h.panels + 3) / 4 * 4;
+  FewArgs o = h;
+  h.X = X;
+  h.ldx = ldx;
+  h.xs = x_scale;
   h.W[0] = up;
   h.ws[0] = up_scale;
   h.ldws[0] = ld_up;
@@ -498,18 +598,35 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   h.d_in = d;
   h.d_out = ff;
   h.nb = (d + WP_BK - 1) / WP_BK;
-  const dim3 hg((unsigned)a.tiles, groups);
-  if (gate) launch_hidden<2>(x_dt, h, hg, stream);
-  else launch_hidden<1>(x_dt, h, hg, stream);
+  if (gate) launch_hidden<2>(x_dt, h, grid(h.panels), stream);
+  else launch_hidden<1>(x_dt, h, grid(h.panels), stream);
   int r = fpi::check_launch("moe_hidden_kernel");
   if (r) return r;
-  a.W[0] = down;
-  a.ws[0] = down_scale;
-  a.ldws[0] = ld_down;
-  a.d_in = ff;
-  a.d_out = d;
-  a.nb = (ff + WP_BK - 1) / WP_BK;
-  moe_output_kernel<<<dim3((unsigned)a.n_count, groups), dim3(NT), 0, stream>>>(a);
+  o.X = o.A;
+  o.ldx = o.lda;
+  o.W[0] = down;
+  o.ws[0] = down_scale;
+  o.ldws[0] = ld_down;
+  o.d_in = ff;
+  o.d_out = d;
+  o.nb = (ff + WP_BK - 1) / WP_BK;
+  o.part = (float*)(w + s.part);
+  o.weights = weights;
+  o.Y = Y;
+  o.ldy = ldy;
+  o.y_dt = y_dt;
+  o.panels = o.n_count;
+  x_dt = few ? FP_F32 : FP_I8;
+  const dim3 og = grid(o.panels);
+  if (few) {
+    moe_output_kernel<float><<<og, dim3(NT), 0, stream>>>(o);
+  } else {
+    r = fp_quantize_rows(FP_F32, o.A, o.lda, T * K, ff, (int8_t*)(w + s.aq), o.lda, (float*)(w + s.as), stream);
+    if (r) return r;
+    o.X = w + s.aq;
+    o.xs = (const float*)(w + s.as);
+    moe_output_kernel<int8_t><<<og, dim3(NT), 0, stream>>>(o);
+  }
   r = fpi::check_launch("moe_output_kernel");
   return r ? r : fpi::ok();
 }
