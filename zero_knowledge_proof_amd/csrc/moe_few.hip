@@ -15,11 +15,12 @@
 // takes an equal range of them, whatever the ids say: it reads the ids, finds its
 // experts and their tokens, quantizes the tokens' rows as it multiplies and keeps
 // its weights' loads going from panel to panel. The first launch leaves a (fp32)
-// with each panel's largest magnitude, from which the second has a row's scale;
-// in the second, the last workgroup to arrive at 32 outputs adds the experts'
-// parts of every token in the order of its choices. For more than FEW tokens,
-// whose rows an expert's workgroups would each quantize again, two launches
-// between do that once.
+// with each panel's largest magnitude, from which the second has a row's scale.
+// The second cuts its ranges inside panels: the parts of a product are added as
+// integers, in any order, and the last workgroup to arrive at 32 outputs scales
+// and adds the experts' products of every token in the order of its choices. For
+// more than FEW tokens, whose rows an expert's workgroups would each quantize
+// again, two launches between do that once.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
@@ -29,7 +30,6 @@
 
 namespace {
 
-constexpr int NW = 4, NT = NW * 64;       // waves, each with units of K in turn
 constexpr int SLOTS = FP_MAX_FEW_SLOTS;   // T K
 constexpr int FEW = 8;                    // tokens whose rows are quantized where they are multiplied
 constexpr int RP = 36;                    // LDS words of a row's sums
@@ -62,18 +62,21 @@ struct FewArgs {
   int64_t lda;
   float* top;                  // [slots][ldt]: largest magnitude of each panel of ff, then zeros to whole pieces
   int32_t ldt;
-  uint32_t* count;             // arrivals at each 32 outputs
-  float* part;                 // [slots][d]: D a_s
+  int32_t* zero;               // count and part, which the first launch clears
+  int64_t n_zero;
+  uint32_t* count;             // arrivals at each 32 outputs, in units
+  int32_t* part;               // [slots][d]: the products of a_s and D
+  float* xs_out;               // [slots][panels]: the scales of the rows a_s
   const float* weights;        // [T][K]
   void* Y;
   int64_t ldy;
-  int32_t y_dt, n_count;
+  int32_t y_dt;
 };
 
 template <typename XT>
 constexpr int rows_of() { return sizeof(XT) == 1 ? 32 : 8; }  // of an expert at a time: 8 where they are quantized here
-template <typename XT>
-constexpr int wgs_of() { return sizeof(XT) == 1 ? 3 : 4; }  // workgroups that a CU holds
+constexpr int NW = 4, NT = NW * 64;  // waves, each with units of K in turn
+constexpr int WGS = 3;               // workgroups that a CU holds
 constexpr int CUS = 256;
 
 // A unit of K: the blocks of it that a wave takes together, 8 KiB of weights (4
@@ -83,8 +86,9 @@ struct Unit {
   static constexpr int BLOCKS = ROWS == 8 ? 4 / MAPS : 2, K = BLOCKS * WP_BK, PIECES = K / 128, XP = K + 16;
 };
 
-template <int MAPS, int ROWS>
+template <int MAPS, typename XT>
 struct Lds {
+  static constexpr int ROWS = rows_of<XT>();
   __attribute__((aligned(16))) int8_t x[NW][ROWS * Unit<MAPS, ROWS>::XP];  // a wave's rows
   __attribute__((aligned(16))) int32_t red[NW][ROWS * RP];           // the waves' sums
   uint16_t id[SLOTS], list[SLOTS];                                   // the slots' experts (NONE: no expert); an expert's slots
@@ -152,6 +156,7 @@ __device__ __forceinline__ void row_scales(int nr, int64_t d, Row row, L& lds) {
   constexpr int EV = 16 / (int)sizeof(F);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int cut = nr <= 1 ? 4 : (nr <= 2 ? 2 : 1), part = wave % cut;
+  static_assert(NW == 4, "a row is cut over four waves at most");
   __syncthreads();  // the last rows' scales are read
   for (int r = wave / cut; r < nr; r += NW / cut) {
     const F* p = row(r);
@@ -194,7 +199,6 @@ __device__ __forceinline__ void row_scales(int nr, int64_t d, Row row, L& lds) {
   }
   __syncthreads();
 }
-static_assert(NW == 4, "row_scales cuts a row over four waves at most");
 
 // sdev::quantize of four values, as the bytes of a word. 1.5 2^23 added to a value
 // of at most 127 rounds it to the nearest, ties to even, and leaves it in the low
@@ -248,16 +252,24 @@ struct Piece {
   }
 };
 
-// The products of nr rows (at most ROWS; row(i) their addresses) with the panels
-// [t0, t1) of MAPS matrices: for each panel done(panel, z), where z[map][m] of
-// thread tid is the integer product of row tid / 32 + (NT / 32) m and the panel's
-// output tid % 32. Wave w takes units w, w + NW, ... of K. Loads return in the
-// order in which they were issued: a unit's rows go before its weights, and both
-// as soon as the unit before them is multiplied, over the panels' ends.
-template <int MAPS, typename XT, bool WHOLE, typename Row, typename L, typename Done>
-__device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MAPS], int t0, int t1, int nr, Row row, L& lds,
-                                         Done done) {
-  constexpr int ROWS = rows_of<XT>();
+// A range of units, [from, to) of a stream in which panel t has [t NU, (t + 1) NU).
+struct Range {
+  int64_t from, to;
+};
+
+// The products of nr rows (at most ROWS; row(i) their addresses) with a range of
+// the panels of MAPS matrices: for each panel of it begin(panel), which may load
+// what the products hide, and done(panel, whole, z), where `whole` says that the
+// range has all of the panel and
+// z[map][m] of thread tid is the integer product of row tid / 32 + (NT / 32) m and
+// the panel's output tid % 32 over the range's units of the panel. The waves take
+// these in turn. Loads return in the order in which they were issued: a unit's
+// rows go before its weights, and both as soon as the unit before them is
+// multiplied, over the panels' ends; the first go while scales() finds the rows'.
+template <int MAPS, typename XT, bool WHOLE, typename Row, typename Scales, typename L, typename Begin, typename Done>
+__device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MAPS], const Range& range, int nr, Row row,
+                                         Scales scales, L& lds, Begin begin, Done done) {
+  constexpr int ROWS = L::ROWS;
   using U = Unit<MAPS, ROWS>;
   constexpr int XR = ROWS / 8, ZR = (ROWS + NT / 32 - 1) / (NT / 32);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -288,18 +300,30 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
           wf[i][b][q] = *(const __attribute__((address_space(1))) v4i*)(pw + (int64_t)min(U::BLOCKS * u + b, NB - 1) * (WP_BK * 32) + 1024 * q + lane * 16);
     }
   };
-  sdev::RowScale rs{};
-  if constexpr (sizeof(XT) > 1) rs = lds.rs[lane >> 3];
   int8_t* xs = lds.x[wave] + (lane >> 3) * U::XP + kc;
   const int8_t* xf = lds.x[wave] + (r & (ROWS - 1)) * U::XP + 32 * h;  // fragments
-  if (wave < NU) load(t0, wave);
+  const int t0 = (int)(range.from / NU), t1 = (int)((range.to + NU - 1) / NU);
+  const int first = (int)(range.from - (int64_t)t0 * NU), last = (int)(range.to - (int64_t)(t1 - 1) * NU);
+  auto start = [&](int t) { return (t == t0 ? first : 0) + wave; };
+  auto limit = [&](int t) { return t == t1 - 1 ? last : NU; };
+  // the wave's first unit of panel t or, where it has none there, of a later one
+  auto load_from = [&](int t) {
+    for (; t < t1; ++t)
+      if (start(t) < limit(t)) return load(t, start(t));
+  };
+  load_from(t0);
+  scales();
+  sdev::RowScale rs{};
+  if constexpr (sizeof(XT) > 1) rs = lds.rs[lane >> 3];
   for (int t = t0; t < t1; ++t) {
+    begin(t);
     v16i acc[MAPS];
 #pragma unroll
     for (int i = 0; i < MAPS; ++i)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][v] = 0;
-    for (int u = wave; u < NU; u += NW) {
+    const int end = limit(t);
+    for (int u = start(t); u < end; u += NW) {
 #pragma unroll
       for (int c = 0; c < XR; ++c)
         if (c == 0 || 8 * c < nr)
@@ -315,8 +339,8 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
           for (int i = 0; i < MAPS; ++i) acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i][b][q], f, acc[i], 0, 0, 0);
         }
       }
-      const bool more = u + NW < NU;
-      if (more || t + 1 < t1) load(more ? t : t + 1, more ? u + NW : wave);
+      if (u + NW < end) load(t, u + NW);
+      else load_from(t + 1);
     }
     // lane (row r, h) register 4 g + e: output 8 g + 4 h + e
     int32_t z[MAPS][ZR];
@@ -339,38 +363,56 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
           for (int w = 0; w < NW; ++w) z[i][m] += lds.red[w][tl * RP + tid % 32];
       }
     }
-    done(t, z);
+    done(t, (t > t0 || first == 0) && end == NU, z);
   }
 }
 
-// Where workgroup b's panels begin among all of them.
-__device__ __forceinline__ int64_t share(int64_t all, int b) { return all * b / gridDim.x; }
+// Where the share of `all` of workgroup b of n begins.
+__device__ __forceinline__ int64_t share(int64_t all, int b, int n) { return all * min(b, n) / n; }
+
+// The experts' parts of the stream's range [first, end), with `all` units each, in
+// turn: part(expert, range within it, its number of slots).
+template <typename L, typename Part>
+__device__ __forceinline__ void experts_of(const FewArgs& a, int64_t first, int64_t end, int64_t all, L& lds, Part part) {
+  for (int64_t at = first; at < end;) {
+    const int j = (int)(at / all);
+    const Range range{at - j * all, min(all, end - j * all)};
+    at += range.to - range.from;
+    const int e = __builtin_amdgcn_readfirstlane(lds.met[j]);
+    part(e, range, find_slots(a.ids, e, lds));
+  }
+}
 
 template <int MAPS, typename XT, bool WHOLE>
-__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_hidden_kernel(FewArgs a) {
-  constexpr int ROWS = rows_of<XT>();
-  __shared__ Lds<MAPS, ROWS> lds;
+__global__ __launch_bounds__(NT, WGS) void moe_hidden_kernel(FewArgs a) {
+  using L = Lds<MAPS, XT>;
+  constexpr int ROWS = L::ROWS;
+  __shared__ L lds;
   const int tid = threadIdx.x;
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.n_count; i += NT) a.count[i] = 0;
-  const int64_t all = (int64_t)find_experts(a.ids, lds) * a.panels, end = share(all, blockIdx.x + 1);
-  for (int64_t at = share(all, blockIdx.x); at < end;) {
-    const int j = (int)(at / a.panels), t0 = (int)(at - (int64_t)j * a.panels);
-    const int t1 = (int)min((int64_t)a.panels, t0 + end - at);
-    at += t1 - t0;
-    const int e = __builtin_amdgcn_readfirstlane(lds.met[j]), n = find_slots(a.ids, e, lds);
+  // what the outputs' launch counts and adds up from zero
+  for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < a.n_zero; i += (int64_t)gridDim.x * NT) a.zero[i] = 0;
+  const int present = find_experts(a.ids, lds), NU = (a.nb + Unit<MAPS, ROWS>::BLOCKS - 1) / Unit<MAPS, ROWS>::BLOCKS;
+  if (present == 0) return;
+  const int64_t panels = (int64_t)present * a.panels;
+  const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, panels);
+  experts_of(a, share(panels, b, wgs) * NU, share(panels, b + 1, wgs) * NU, (int64_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
     Weights W[MAPS];
 #pragma unroll
     for (int i = 0; i < MAPS; ++i) W[i] = (Weights)a.W[i][e];
     for (int r0 = 0; r0 < n; r0 += ROWS) {
       const int nr = min(n - r0, ROWS);
       auto row = [&](int r) { return (const XT*)a.X + (int64_t)((uint32_t)lds.list[r0 + r] / (uint32_t)a.ids.K) * a.ldx; };
-      if constexpr (sizeof(XT) > 1) row_scales<XT, WHOLE>(nr, a.d_in, row, lds);
-      products<MAPS, XT, WHOLE>(a, W, t0, t1, nr, row, lds, [&](int t, const auto& z) {
+      auto scales = [&]() {
+        if constexpr (sizeof(XT) > 1) row_scales<XT, WHOLE>(nr, a.d_in, row, lds);
+      };
+      float ws[MAPS];
+      auto begin = [&](int t) {
         const int o = t * 32 + tid % 32;
-        float ws[MAPS];
 #pragma unroll
         for (int i = 0; i < MAPS; ++i) ws[i] = tid / 32 < nr && o < a.d_out ? a.ws[i][e * a.ldws[i] + o] : 0.f;
+      };
+      products<MAPS, XT, WHOLE>(a, W, range, nr, row, scales, lds, begin, [&](int t, bool, const auto& z) {
+        const int o = t * 32 + tid % 32;
 #pragma unroll
         for (int m = 0; m < (int)(sizeof(z[0]) / 4); ++m) {
           const int tl = tid / 32 + NT / 32 * m;
@@ -395,7 +437,7 @@ __global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_hidden_kernel(FewArgs a)
         }
       });
     }
-  }
+  });
 }
 
 __device__ __forceinline__ void store_out(const FewArgs& a, int t, int o, float f) {
@@ -405,57 +447,82 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int o, float 
 }
 
 // Rows of XT = float are A's own, with scales from a.top, int8 ones those in X
-// with a.xs.
+// with a.xs. Uncut products go to `part` scaled, cut ones as integers, with the
+// rows' scales.
 template <typename XT>
-__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a) {
-  constexpr int ROWS = rows_of<XT>();
-  __shared__ Lds<1, ROWS> lds;
+__global__ __launch_bounds__(NT, WGS) void moe_output_kernel(FewArgs a) {
+  using L = Lds<1, XT>;
+  constexpr int ROWS = L::ROWS;
+  __shared__ L lds;
   const int tid = threadIdx.x;
-  const int present = find_experts(a.ids, lds);
+  const int present = find_experts(a.ids, lds), NU = (a.nb + Unit<1, ROWS>::BLOCKS - 1) / Unit<1, ROWS>::BLOCKS;
   if (present == 0) {  // no token has an expert
     for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < (int64_t)a.ids.T * a.d_out; i += (int64_t)gridDim.x * NT)
       store_out(a, (int)(i / a.d_out), (int)(i % a.d_out), 0.f);
     return;
   }
-  const int64_t all = (int64_t)present * a.panels, first = share(all, blockIdx.x), end = share(all, blockIdx.x + 1);
+  // Whole panels for every workgroup, or parts of panels where whole ones would
+  // leave many workgroups idle and the parts are worth their additions: with fewer
+  // panels than CUs, or with a last round that few workgroups have.
+  const int64_t panels = (int64_t)present * a.panels, all = panels * NU;
+  const int64_t rounds = (panels + gridDim.x - 1) / gridDim.x;
+  const bool cut = NU >= 2 * NW && (panels < CUS || (rounds > 1 && panels * 10 < rounds * gridDim.x * 9));
+  const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, cut ? all / (2 * NW) : panels);
+  const int64_t first = cut ? share(all, b, wgs) : share(panels, b, wgs) * NU;
+  const int64_t end = cut ? share(all, b + 1, wgs) : share(panels, b + 1, wgs) * NU;
   if (first == end) return;
-  for (int64_t at = first; at < end;) {
-    const int j = (int)(at / a.panels), t0 = (int)(at - (int64_t)j * a.panels);
-    const int t1 = (int)min((int64_t)a.panels, t0 + end - at);
-    at += t1 - t0;
-    const int e = __builtin_amdgcn_readfirstlane(lds.met[j]), n = find_slots(a.ids, e, lds);
+  experts_of(a, first, end, (int64_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
     const Weights W[1] = {(Weights)a.W[0][e]};
     for (int r0 = 0; r0 < n; r0 += ROWS) {
       const int nr = min(n - r0, ROWS);
       auto row = [&](int r) { return (const XT*)a.X + (int64_t)lds.list[r0 + r] * a.ldx; };
-      if constexpr (sizeof(XT) > 1)
-        row_scales<float, true>(nr, a.ldt, [&](int r) { return a.top + (int64_t)lds.list[r0 + r] * a.ldt; }, lds);
-      products<1, XT, true>(a, W, t0, t1, nr, row, lds, [&](int t, const auto& z) {
+      auto scales = [&]() {
+        if constexpr (sizeof(XT) > 1) {
+          row_scales<float, true>(nr, a.ldt, [&](int r) { return a.top + (int64_t)lds.list[r0 + r] * a.ldt; }, lds);
+        }
+      };
+      float ws = 0.f;
+      auto begin = [&](int t) {
         const int o = t * 32 + tid % 32;
-        const float ws = tid / 32 < nr && o < a.d_out ? a.ws[0][e * a.ldws[0] + o] : 0.f;
+        if (!cut && tid / 32 < nr && o < a.d_out) ws = a.ws[0][e * a.ldws[0] + o];
+      };
+      products<1, XT, true>(a, W, range, nr, row, scales, lds, begin, [&](int t, bool whole, const auto& z) {
+        const int o = t * 32 + tid % 32;
 #pragma unroll
         for (int m = 0; m < (int)(sizeof(z[0]) / 4); ++m) {
           const int tl = tid / 32 + NT / 32 * m;
           if (tl >= nr || o >= a.d_out) continue;
           const int slot = lds.list[r0 + tl];
+          int32_t* const p = &a.part[(int64_t)slot * a.d_out + o];
           float xs;
           if constexpr (sizeof(XT) > 1) xs = lds.rs[tl].scale;
           else xs = a.xs[slot];
-          __hip_atomic_store(&a.part[(int64_t)slot * a.d_out + o], (float)z[0][m] * xs * ws, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          if (!cut) {
+            __hip_atomic_store((float*)p, (float)z[0][m] * xs * ws, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            continue;
+          }
+          if (whole) __hip_atomic_store(p, z[0][m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          else __hip_atomic_fetch_add(p, z[0][m], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          // (one to a panel: all workgroups of an expert writing one and the same took 17 us)
+          if (tid % 32 == 0) __hip_atomic_store(&a.xs_out[(int64_t)slot * a.panels + t], xs, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       });
     }
-  }
-  // each thread's stores are at the agent's level before its workgroup's arrivals count
+  });
+  // each thread's additions are at the agent's level before its workgroup's arrivals count
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_s_waitcnt(0);
-  for (int64_t base = first; base < end; base += NT) {
+  const uint32_t units = (uint32_t)present * NU;  // of 32 outputs, in all experts
+  const int64_t p0 = first / NU, p1 = (end + NU - 1) / NU;
+  for (int64_t base = p0; base < p1; base += NT) {
     __syncthreads();
     if (tid == 0) lds.last = 0;
     __syncthreads();
-    if (base + tid < end) {
-      const int t = (int)((base + tid) % a.panels);
-      if (__hip_atomic_fetch_add(&a.count[t], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == (uint32_t)present)
+    const int64_t p = base + tid;
+    if (p < p1) {
+      const int t = (int)(p % a.panels);
+      const uint32_t mine = (uint32_t)(min(end, (p + 1) * NU) - max(first, p * NU));
+      if (__hip_atomic_fetch_add(&a.count[t], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine == units)
         lds.tile[atomicAdd(&lds.last, 1)] = (uint16_t)t;
     }
     __syncthreads();
@@ -466,17 +533,26 @@ __global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a)
       constexpr int KG = 8;  // choices whose loads are under way together
       float y = 0.f;
       for (int k0 = 0; k0 < a.ids.K; k0 += KG) {
-        float w[KG], v[KG];
+        float w[KG], xs[KG], ws[KG];
+        int32_t z[KG];
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
           const int s = t * a.ids.K + min(k0 + k, a.ids.K - 1);
           w[k] = a.weights[s];
-          // (a slot without an expert has an element here too, which nothing wrote)
-          v[k] = __hip_atomic_load(&a.part[(int64_t)s * a.d_out + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          z[k] = __hip_atomic_load(&a.part[(int64_t)s * a.d_out + o], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (cut) {
+#pragma unroll
+          for (int k = 0; k < KG; ++k) {  // (a slot without an expert has places here too, which nothing wrote)
+            const int s = t * a.ids.K + min(k0 + k, a.ids.K - 1), e = lds.id[s];
+            xs[k] = __hip_atomic_load(&a.xs_out[(int64_t)s * a.panels + o / 32], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            ws[k] = a.ws[0][(e == NONE ? 0 : e) * a.ldws[0] + o];
+          }
         }
 #pragma unroll
         for (int k = 0; k < KG; ++k)
-          if (k0 + k < a.ids.K && lds.id[t * a.ids.K + k0 + k] != NONE) y = __builtin_fmaf(w[k], v[k], y);
+          if (k0 + k < a.ids.K && lds.id[t * a.ids.K + k0 + k] != NONE)
+            y = __builtin_fmaf(w[k], cut ? (float)z[k] * xs[k] * ws[k] : __int_as_float(z[k]), y);
       }
       store_out(a, t, o, y);
     }
@@ -486,16 +562,16 @@ __global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a)
 int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
 
 struct Scratch {
-  size_t top, A, part, xs, xq, as, aq, bytes;  // xs.. aq: int8 rows, with more than FEW tokens
+  size_t A, part, xs_out, top, xs, xq, as, aq, bytes;
 };
 int64_t chunked(int64_t n) { return (n + 15) / 16 * 16; }
 Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
   Scratch s{};
   size_t at = 0;
   auto take = [&](int64_t bytes) { const size_t p = at; at += fpi::align_up((size_t)bytes, 256); return p; };
-  take((d + 31) / 32 * 4);  // arrivals
+  s.part = take(((d + 31) / 32 + N * d) * 4);  // behind the arrivals
   s.A = take(N * chunked(ff) * 4);
-  s.part = take(N * d * 4);
+  s.xs_out = take(N * ((d + 31) / 32) * 4);
   if (T <= FEW) {
     s.top = take(N * ((ff + 127) / 128 * 4) * 4);
   } else {
@@ -516,17 +592,29 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t d, int32_t ff) {
   return FP_OK;
 }
 
+// As many workgroups as the GPU holds at once, if the experts that the tokens can
+// meet have `parts` for them.
+dim3 few_grid(int64_t parts) {
+  const int64_t held = CUS * WGS;
+  return dim3((unsigned)(parts < held ? parts : held));
+}
 template <int MAPS, typename XT>
-void launch_hidden_rows(const FewArgs& a, dim3 grid, hipStream_t st) {
-  if (a.d_in % 16 == 0) moe_hidden_kernel<MAPS, XT, true><<<grid, dim3(NT), 0, st>>>(a);
-  else moe_hidden_kernel<MAPS, XT, false><<<grid, dim3(NT), 0, st>>>(a);
+void launch_hidden_rows(const FewArgs& a, int64_t most, bool whole, hipStream_t st) {
+  const dim3 grid = few_grid(most * a.panels), block(NT);
+  if (whole) moe_hidden_kernel<MAPS, XT, true><<<grid, block, 0, st>>>(a);
+  else moe_hidden_kernel<MAPS, XT, false><<<grid, block, 0, st>>>(a);
 }
 template <int MAPS>
-void launch_hidden(int x_dt, const FewArgs& a, dim3 grid, hipStream_t st) {
-  if (x_dt == FP_I8) launch_hidden_rows<MAPS, int8_t>(a, grid, st);
-  else if (x_dt == FP_F32) launch_hidden_rows<MAPS, float>(a, grid, st);
-  else if (x_dt == FP_F16) launch_hidden_rows<MAPS, __half>(a, grid, st);
-  else launch_hidden_rows<MAPS, __hip_bfloat16>(a, grid, st);
+void launch_hidden(int x_dt, const FewArgs& a, int64_t most, bool whole, hipStream_t st) {
+  if (x_dt == FP_I8) launch_hidden_rows<MAPS, int8_t>(a, most, whole, st);
+  else if (x_dt == FP_F32) launch_hidden_rows<MAPS, float>(a, most, whole, st);
+  else if (x_dt == FP_F16) launch_hidden_rows<MAPS, __half>(a, most, whole, st);
+  else launch_hidden_rows<MAPS, __hip_bfloat16>(a, most, whole, st);
+}
+template <typename XT>
+void launch_output(const FewArgs& a, int64_t most, hipStream_t st) {
+  const int64_t units = (a.nb + Unit<1, rows_of<XT>()>::BLOCKS - 1) / Unit<1, rows_of<XT>()>::BLOCKS;
+  moe_output_kernel<XT><<<few_grid(most * a.panels * units), dim3(NT), 0, st>>>(a);
 }
 
 }  // namespace
@@ -563,6 +651,7 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   if ((uintptr_t)ws % 256) return fpi::fail(FP_EARG, "%s: workspace not 256-byte aligned", fn);
   char* const w = (char*)ws;
   const bool few = T <= FEW;
+  bool whole = d % 16 == 0;
   if (!few && x_dt != FP_I8) {
     const int r = fp_quantize_rows(x_dt, X, ldx, T, d, (int8_t*)(w + s.xq), chunked(d), (float*)(w + s.xs), stream);
     if (r) return r;
@@ -570,16 +659,13 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
     X = w + s.xq;
     ldx = chunked(d);
     x_scale = (const float*)(w + s.xs);
+    whole = true;
   }
   const int64_t most = T * K < E ? T * K : E;  // experts that the tokens can meet
-  auto grid = [&](int64_t panels) {  // as many workgroups as the GPU holds at once
-    const int64_t held = CUS * (x_dt == FP_I8 ? wgs_of<int8_t>() : wgs_of<float>());
-    return dim3((unsigned)(most * panels < held ? most * panels : held));
-  };
   FewArgs h{};
   h.ids = Ids{ids, id_bytes == 8, T, K, E};
-  h.count = (uint32_t*)w;
-  h.n_count = (d + 31) / 32;
+  h.zero = (int32_t*)(w + s.part);
+  h.n_zero = (d + 31) / 32 + (int64_t)T * K * d;
   h.A = (float*)(w + s.A);
   h.lda = chunked(ff);
   h.top = few ? (float*)(w + s.top) : nullptr;
@@ -598,8 +684,8 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   h.d_in = d;
   h.d_out = ff;
   h.nb = (d + WP_BK - 1) / WP_BK;
-  if (gate) launch_hidden<2>(x_dt, h, grid(h.panels), stream);
-  else launch_hidden<1>(x_dt, h, grid(h.panels), stream);
+  if (gate) launch_hidden<2>(x_dt, h, most, whole, stream);
+  else launch_hidden<1>(x_dt, h, most, whole, stream);
   int r = fpi::check_launch("moe_hidden_kernel");
   if (r) return r;
   o.X = o.A;
@@ -610,22 +696,22 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   o.d_in = ff;
   o.d_out = d;
   o.nb = (ff + WP_BK - 1) / WP_BK;
-  o.part = (float*)(w + s.part);
+  o.panels = (d + 31) / 32;
+  o.count = (uint32_t*)o.zero;
+  o.part = o.zero + o.panels;
+  o.xs_out = (float*)(w + s.xs_out);
   o.weights = weights;
   o.Y = Y;
   o.ldy = ldy;
   o.y_dt = y_dt;
-  o.panels = o.n_count;
-  x_dt = few ? FP_F32 : FP_I8;
-  const dim3 og = grid(o.panels);
   if (few) {
-    moe_output_kernel<float><<<og, dim3(NT), 0, stream>>>(o);
+    launch_output<float>(o, most, stream);
   } else {
     r = fp_quantize_rows(FP_F32, o.A, o.lda, T * K, ff, (int8_t*)(w + s.aq), o.lda, (float*)(w + s.as), stream);
     if (r) return r;
     o.X = w + s.aq;
     o.xs = (const float*)(w + s.as);
-    moe_output_kernel<int8_t><<<og, dim3(NT), 0, stream>>>(o);
+    launch_output<int8_t>(o, most, stream);
   }
   r = fpi::check_launch("moe_output_kernel");
   return r ? r : fpi::ok();
