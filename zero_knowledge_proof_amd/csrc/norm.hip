@@ -42,11 +42,17 @@ struct NormArgs {
   float* scale;
 };
 
-// n (at least 1) elements, whole vectors at any element's address.
-template <typename E>
-__device__ __forceinline__ void store16u(E* p, const v4i& w, int64_t n) {
+// n (at least 1) elements as a vector, at any element's address; WHOLE: n is not
+// less than a vector's, and the code for fewer is left out.
+template <typename E, bool WHOLE>
+__device__ __forceinline__ v4i loadv(const E* p, int64_t n) {
+  if constexpr (WHOLE) return *(const typename sdev::AnyVec<sizeof(E)>::type*)p;
+  else return sdev::load16u(p, n);
+}
+template <typename E, bool WHOLE>
+__device__ __forceinline__ void storev(E* p, const v4i& w, int64_t n) {
   constexpr int EV = 16 / (int)sizeof(E);
-  if (n >= EV) {
+  if (WHOLE || n >= EV) {
     *(typename sdev::AnyVec<sizeof(E)>::type*)p = w;
     return;
   }
@@ -59,14 +65,14 @@ __device__ __forceinline__ void store16u(E* p, const v4i& w, int64_t n) {
 }
 
 // EV consecutive weights, as loaded.
-template <typename W, int EV>
+template <typename W, int EV, bool WHOLE>
 struct Weights {
   static constexpr int N = EV * (int)sizeof(W) / 16;
   v4i raw[N];
   __device__ __forceinline__ void load(const W* p, int64_t n) {
     constexpr int PER = 16 / (int)sizeof(W);
 #pragma unroll
-    for (int i = 0; i < N; ++i) raw[i] = n > i * PER ? sdev::load16u(p + i * PER, n - i * PER) : v4i{0, 0, 0, 0};
+    for (int i = 0; i < N; ++i) raw[i] = n > i * PER ? loadv<W, WHOLE>(p + i * PER, n - i * PER) : v4i{0, 0, 0, 0};
   }
   __device__ __forceinline__ float at(int e) const {
     constexpr int PER = 16 / (int)sizeof(W);
@@ -95,15 +101,15 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
   return v;
 }
 
-// P threads to a row, each with up to NV vectors of it in registers (a longer
-// row's others are read again; only where P is the workgroup).
-template <typename E, typename W, int P, int NV>
-__global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
-  constexpr int EV = 16 / (int)sizeof(E), RPB = NT / P;
-  __shared__ float red[2][2][NT / 64], redo[NT / 64];
+// P threads to a row, each with up to NV vectors of it in registers; from 128
+// threads on a row to a workgroup, which reads a longer row's other vectors again.
+template <typename E, typename W, int P, int NV, bool WHOLE>
+__global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_kernel(NormArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), TB = P > 64 ? P : NT, RPB = TB / P;
+  __shared__ float red[2][2][TB / 64], redo[TB / 64];
   const int l = threadIdx.x % P;
-  Weights<W, EV> w[NV];
-  auto weights = [&](Weights<W, EV>& x, int64_t i) { x.load((const W*)a.w + i * EV, a.d - i * EV); };
+  Weights<W, EV, WHOLE> w[NV];
+  auto weights = [&](Weights<W, EV, WHOLE>& x, int64_t i) { x.load((const W*)a.w + i * EV, a.d - i * EV); };
   if (a.w) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) weights(w[v], v * P + l);
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
     };
     auto again = [&](int64_t i, float* h) {
       const int64_t n = a.d - i * EV;
-      sum(sdev::load16u(x + i * EV, n), a.R ? sdev::load16u(r + i * EV, n) : v4i{0, 0, 0, 0}, h);
+      sum(loadv<E, WHOLE>(x + i * EV, n), a.R ? loadv<E, WHOLE>(r + i * EV, n) : v4i{0, 0, 0, 0}, h);
     };
     float h[NV][EV];
     v4i rx[NV], rr[NV];
@@ -127,8 +133,8 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
       const int64_t n = a.d - (int64_t)(v * P + l) * EV;
       rx[v] = rr[v] = v4i{0, 0, 0, 0};
       if (n > 0) {
-        rx[v] = sdev::load16u(x + (v * P + l) * EV, n);
-        if (a.R) rr[v] = sdev::load16u(r + (v * P + l) * EV, n);
+        rx[v] = loadv<E, WHOLE>(x + (v * P + l) * EV, n);
+        if (a.R) rr[v] = loadv<E, WHOLE>(r + (v * P + l) * EV, n);
       }
     }
     float ss = 0.f;
@@ -138,7 +144,7 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < EV; ++e) ss = __builtin_fmaf(h[v][e], h[v][e], ss);
     }
-    if constexpr (P == NT)
+    if constexpr (P > 64)
       for (int64_t i = NV * P + l; i * EV < a.d; i += P) {
         float f[EV];
         again(i, f);
@@ -159,18 +165,18 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
           const float f = h[v][e] * pre;
           ss = __builtin_fmaf(f, f, ss);
         }
-      if constexpr (P == NT)
+      if constexpr (P > 64)
         for (int64_t i = NV * P + l; i * EV < a.d; i += P) {
           float f[EV];
           again(i, f);
 #pragma unroll
           for (int e = 0; e < EV; ++e) ss = __builtin_fmaf(f[e] * pre, f[e] * pre, ss);
         }
-      if constexpr (P == NT) __syncthreads();  // an earlier row's sums in redo are read
+      if constexpr (P > 64) __syncthreads();  // an earlier row's sums in redo are read
       ss = row_reduce<P, false>(ss, redo);
       s = 1.0f / sqrtf(ss * a.inv_d);
     }
-    auto norm = [&](float f, const Weights<W, EV>& wv, int e) {
+    auto norm = [&](float f, const Weights<W, EV, WHOLE>& wv, int e) {
       const float n = (f * pre) * s;
       return a.w ? n * wv.at(e) : n;
     };
@@ -185,7 +191,7 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int64_t n = a.d - (int64_t)(v * P + l) * EV;
-        if (n > 0) store16u((E*)a.H + t * a.ldh + (v * P + l) * EV, sdev::pack16<E>(h[v]), n);
+        if (n > 0) storev<E, WHOLE>((E*)a.H + t * a.ldh + (v * P + l) * EV, sdev::pack16<E>(h[v]), n);
       }
     }
 #pragma unroll
@@ -197,14 +203,14 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
         h[v][e] = e < n ? y : 0.f;  // past the row: 0 times an s that is NaN or infinite
         see(h[v][e]);
       }
-      if (a.Y && n > 0) store16u((E*)a.Y + t * a.ldy + (v * P + l) * EV, sdev::pack16<E>(h[v]), n);
+      if (a.Y && n > 0) storev<E, WHOLE>((E*)a.Y + t * a.ldy + (v * P + l) * EV, sdev::pack16<E>(h[v]), n);
     }
     sdev::RowScale rs{};
     if (a.Q) {
-      if constexpr (P == NT)
+      if constexpr (P > 64)
         for (int64_t i = NV * P + l; i * EV < a.d; i += P) {
           float f[EV];
-          Weights<W, EV> wv;
+          Weights<W, EV, WHOLE> wv;
           again(i, f);
           if (a.w) weights(wv, i);
 #pragma unroll
@@ -221,7 +227,7 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
       int b[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < EV; ++e) b[e / 4] |= (sdev::quantize(y[e], rs) & 255) << (8 * (e % 4));
-      if (n >= EV) {
+      if (WHOLE || n >= EV) {
         if constexpr (EV == 8) *(sdev::AnyPair*)q = sdev::AnyPair{b[0], b[1]};
         else *(sdev::AnyWord*)q = b[0];
       } else {
@@ -235,17 +241,17 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(NormArgs a) {
       for (int v = 0; v < NV; ++v)
         if ((int64_t)(v * P + l) * EV < a.d) put(h[v], v * P + l);
     }
-    if constexpr (P == NT)
+    if constexpr (P > 64)
       for (int64_t i = NV * P + l; i * EV < a.d; i += P) {
         const int64_t n = a.d - i * EV;
         float f[EV];
-        Weights<W, EV> wv;
+        Weights<W, EV, WHOLE> wv;
         again(i, f);
         if (a.w) weights(wv, i);
-        if (a.H) store16u((E*)a.H + t * a.ldh + i * EV, sdev::pack16<E>(f), n);
+        if (a.H) storev<E, WHOLE>((E*)a.H + t * a.ldh + i * EV, sdev::pack16<E>(f), n);
 #pragma unroll
         for (int e = 0; e < EV; ++e) f[e] = norm(f[e], wv, e);
-        if (a.Y) store16u((E*)a.Y + t * a.ldy + i * EV, sdev::pack16<E>(f), n);
+        if (a.Y) storev<E, WHOLE>((E*)a.Y + t * a.ldy + i * EV, sdev::pack16<E>(f), n);
         if (a.Q) put(f, i);
       }
   }
@@ -269,17 +275,17 @@ struct NormBwdArgs {
 
 constexpr int FT = 16;  // values of a row that a thread has
 
-// P threads to a row, FT values each, and max(P, 256) threads to a workgroup. A
+// P threads to a row, FT values each; a row to a workgroup from 128 threads on. A
 // thread has the same columns in every row that its workgroup takes (a stride of
 // the grid apart), so the columns' dw stay in its registers; a workgroup's sums
 // go to a row of `part`.
-template <typename E, typename W, int P>
-__global__ __launch_bounds__(P > NT ? P : NT) void rms_norm_backward_kernel(NormBwdArgs a) {
-  constexpr int EV = 16 / (int)sizeof(E), NV = FT / EV, TB = P > NT ? P : NT, RPB = TB / P;
+template <typename E, typename W, int P, bool WHOLE>
+__global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_backward_kernel(NormBwdArgs a) {
+  constexpr int EV = 16 / (int)sizeof(E), NV = FT / EV, TB = P > 64 ? P : NT, RPB = TB / P;
   __shared__ float red[2][2][TB / 64], redo[2][TB / 64];
   __shared__ float cols[RPB > 1 ? RPB * P * FT : 1];
   const int l = threadIdx.x % P;
-  Weights<W, EV> w[NV];
+  Weights<W, EV, WHOLE> w[NV];
   float dw[NV][EV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -295,9 +301,9 @@ __global__ __launch_bounds__(P > NT ? P : NT) void rms_norm_backward_kernel(Norm
       const int at = (v * P + l) * EV, n = a.d - at;
       rh[v] = ry[v] = rd[v] = v4i{0, 0, 0, 0};
       if (n > 0) {
-        rh[v] = sdev::load16u((const E*)a.H + t * a.ldh + at, n);
-        ry[v] = sdev::load16u((const E*)a.dY + t * a.lddy + at, n);
-        if (a.dH) rd[v] = sdev::load16u((const E*)a.dH + t * a.lddh + at, n);
+        rh[v] = loadv<E, WHOLE>((const E*)a.H + t * a.ldh + at, n);
+        ry[v] = loadv<E, WHOLE>((const E*)a.dY + t * a.lddy + at, n);
+        if (a.dH) rd[v] = loadv<E, WHOLE>((const E*)a.dH + t * a.lddh + at, n);
       }
     }
     auto g = [&](int v, int e) {
@@ -345,7 +351,7 @@ __global__ __launch_bounds__(P > NT ? P : NT) void rms_norm_backward_kernel(Norm
         dw[v][e] = __builtin_fmaf(load_elem<E>(ry[v], e), n, dw[v][e]);
       }
       const int at = (v * P + l) * EV, n = a.d - at;
-      if (n > 0) store16u((E*)a.dX + t * a.lddx + at, sdev::pack16<E>(dx), n);
+      if (n > 0) storev<E, WHOLE>((E*)a.dX + t * a.lddx + at, sdev::pack16<E>(dx), n);
     }
   }
   if (!a.part) return;
@@ -415,18 +421,27 @@ int check_rows(const char* fn, const void* p, int64_t ld, int32_t T, int32_t d, 
   return FP_OK;
 }
 
-template <typename E, typename W>
-void launch_norm(const NormArgs& a, hipStream_t st) {
+template <typename E, typename W, bool WHOLE>
+void launch_norm_whole(const NormArgs& a, hipStream_t st) {
   constexpr int EV = 16 / (int)sizeof(E);
   const int64_t vecs = ((int64_t)a.d + EV - 1) / EV;
   auto grid = [&](int rows) {
     const int64_t n = ((int64_t)a.T + rows - 1) / rows;
     return dim3((unsigned)(n < 2048 ? n : 2048));
   };
-  if (vecs <= 32) rms_norm_kernel<E, W, 16, 2><<<grid(NT / 16), dim3(NT), 0, st>>>(a);
-  else if (vecs <= 128) rms_norm_kernel<E, W, 64, 2><<<grid(NT / 64), dim3(NT), 0, st>>>(a);
-  else if (vecs <= 2 * NT) rms_norm_kernel<E, W, NT, 2><<<grid(1), dim3(NT), 0, st>>>(a);
-  else rms_norm_kernel<E, W, NT, 4><<<grid(1), dim3(NT), 0, st>>>(a);
+  if (vecs <= 32) rms_norm_kernel<E, W, 16, 2, WHOLE><<<grid(NT / 16), dim3(NT), 0, st>>>(a);
+  else if (vecs <= 128) rms_norm_kernel<E, W, 64, 2, WHOLE><<<grid(NT / 64), dim3(NT), 0, st>>>(a);
+  else if (vecs <= 512) rms_norm_kernel<E, W, 256, 2, WHOLE><<<grid(1), dim3(256), 0, st>>>(a);
+  // few rows, for the latency (one of 5120 bf16 with everything: 6.3 us, with 256 threads 7.0)
+  else if (vecs <= 1024 && a.T <= 64) rms_norm_kernel<E, W, 512, 2, WHOLE><<<grid(1), dim3(512), 0, st>>>(a);
+  else if (vecs <= 1024) rms_norm_kernel<E, W, 256, 4, WHOLE><<<grid(1), dim3(256), 0, st>>>(a);
+  else rms_norm_kernel<E, W, 512, 4, WHOLE><<<dim3((unsigned)(a.T < 512 ? a.T : 512)), dim3(512), 0, st>>>(a);
+}
+
+template <typename E, typename W>
+void launch_norm(const NormArgs& a, hipStream_t st) {
+  if (a.d % (16 / (int)sizeof(E)) == 0) launch_norm_whole<E, W, true>(a, st);
+  else launch_norm_whole<E, W, false>(a, st);
 }
 
 int launch_norm_types(fp_dtype dt, fp_dtype w_dt, const NormArgs& a, hipStream_t st) {
@@ -440,23 +455,38 @@ int launch_norm_types(fp_dtype dt, fp_dtype w_dt, const NormArgs& a, hipStream_t
 }
 
 // Threads to a row of the backward pass, and its workgroups.
-int bwd_threads(int32_t d) { return d <= 16 * FT ? 16 : (d <= 64 * FT ? 64 : (d <= 256 * FT ? 256 : 1024)); }
+int bwd_threads(int32_t d) {
+  int p = 16;
+  while (p * FT < d) p *= p == 16 ? 4 : 2;
+  return p;
+}
 int32_t bwd_blocks(int32_t T, int32_t d) {
-  const int p = bwd_threads(d), rows = p < NT ? NT / p : 1;
+  const int p = bwd_threads(d), rows = p <= 64 ? NT / p : 1;
   const int64_t n = ((int64_t)T + rows - 1) / rows;
-  const int64_t most = p > NT ? 256 : 768;
+  // Eight waves a CU: each row of `part` is written and read again (8192 x 4096 bf16
+  // with dh 58.5 us, with four 77, six 62, twelve 65, sixteen 71; the next row loaded
+  // ahead 59).
+  const int64_t most = p == 1024 ? 256 : 256 * 8 * 64 / (p <= 64 ? NT : p);
   return (int32_t)(n < most ? n : most);
+}
+
+template <typename E, typename W, bool WHOLE>
+void launch_bwd_whole(const NormBwdArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)bwd_blocks(a.T, a.d));
+  switch (bwd_threads(a.d)) {
+    case 16: return rms_norm_backward_kernel<E, W, 16, WHOLE><<<grid, dim3(NT), 0, st>>>(a);
+    case 64: return rms_norm_backward_kernel<E, W, 64, WHOLE><<<grid, dim3(NT), 0, st>>>(a);
+    case 128: return rms_norm_backward_kernel<E, W, 128, WHOLE><<<grid, dim3(128), 0, st>>>(a);
+    case 256: return rms_norm_backward_kernel<E, W, 256, WHOLE><<<grid, dim3(256), 0, st>>>(a);
+    case 512: return rms_norm_backward_kernel<E, W, 512, WHOLE><<<grid, dim3(512), 0, st>>>(a);
+    default: return rms_norm_backward_kernel<E, W, 1024, WHOLE><<<grid, dim3(1024), 0, st>>>(a);
+  }
 }
 
 template <typename E, typename W>
 void launch_bwd(const NormBwdArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)bwd_blocks(a.T, a.d));
-  switch (bwd_threads(a.d)) {
-    case 16: return rms_norm_backward_kernel<E, W, 16><<<grid, dim3(NT), 0, st>>>(a);
-    case 64: return rms_norm_backward_kernel<E, W, 64><<<grid, dim3(NT), 0, st>>>(a);
-    case 256: return rms_norm_backward_kernel<E, W, 256><<<grid, dim3(NT), 0, st>>>(a);
-    default: return rms_norm_backward_kernel<E, W, 1024><<<grid, dim3(1024), 0, st>>>(a);
-  }
+  if (a.d % (16 / (int)sizeof(E)) == 0) launch_bwd_whole<E, W, true>(a, st);
+  else launch_bwd_whole<E, W, false>(a, st);
 }
 
 }  // namespace
