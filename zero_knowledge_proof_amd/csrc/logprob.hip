@@ -99,21 +99,30 @@ __device__ __forceinline__ void wave_sync() {
 
 // A wave's keys in LDS.
 struct Keys {
-  __attribute__((aligned(16))) uint64_t at[CAP + 8], lane[64];
+  __attribute__((aligned(16))) uint64_t at[CAP + 16];
   uint64_t best[FP_MAX_TOP];
 };
 
-// How many of m keys, which zeros follow to a multiple of eight, are greater.
+// How many of m keys, which zeros follow to a multiple of sixteen, are greater.
 __device__ __forceinline__ int greater(const uint64_t* key, int m, uint64_t mine) {
   typedef unsigned long long Two __attribute__((ext_vector_type(2)));
   int r = 0;
-  for (int j = 0; j < m; j += 8) {
-    Two x[4];
+  for (int j = 0; j < m; j += 16) {
+    Two x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = *(const Two*)&key[j + 2 * i];
+    for (int i = 0; i < 8; ++i) x[i] = *(const Two*)&key[j + 2 * i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r += (x[i][0] > mine) + (x[i][1] > mine);
+    for (int i = 0; i < 8; ++i) r += (x[i][0] > mine) + (x[i][1] > mine);
   }
+  return r;
+}
+
+// How many of n <= 32 keys in descending order are greater.
+__device__ __forceinline__ int greater_sorted(const uint64_t* key, int n, uint64_t mine) {
+  int r = 0;
+#pragma unroll
+  for (int step = 32; step; step >>= 1)
+    if (r + step <= n && key[r + step - 1] > mine) r += step;
   return r;
 }
 
@@ -123,9 +132,10 @@ __device__ __forceinline__ int greater(const uint64_t* key, int m, uint64_t mine
 struct Top {
   Keys* c;
   int k, n;
+  bool sorted;
   uint64_t lim;  // lesser keys are not among them
-  float least;   // their values' bound
-  __device__ __forceinline__ Top(Keys* c_, int k_) : c(c_), k(k_), n(0), lim(0), least(-__builtin_inff()) {}
+  float least;   // their values' bound; -infinity is none of them
+  __device__ __forceinline__ Top(Keys* c_, int k_) : c(c_), k(k_), n(0), sorted(true), lim(0), least(-__FLT_MAX__) {}
   __device__ __forceinline__ void bound(uint64_t l) {
     if (l <= lim) return;
     lim = l;
@@ -133,8 +143,9 @@ struct Top {
   }
   // the candidates to the k greatest in descending order, by counting for each how many are greater
   __device__ __forceinline__ void sort() {
+    if (sorted) return;
     const int lane = threadIdx.x & 63;
-    if (lane < 8) c->at[n + lane] = 0;
+    if (lane < 16) c->at[n + lane] = 0;
     wave_sync();
     for (int i = lane; i < n; i += 64) {
       const uint64_t mine = c->at[i];
@@ -146,6 +157,7 @@ struct Top {
     if (lane < n) c->at[lane] = c->best[lane];
     wave_sync();
     if (n == k) bound(fpi::readlane_u64(c->best[k - 1], 0) + 1);
+    sorted = true;
   }
   // room for `more` keys, at most CAP - FP_MAX_TOP
   __device__ __forceinline__ void room(int more) {
@@ -153,20 +165,24 @@ struct Top {
   }
   __device__ __forceinline__ void offer(uint64_t key, bool in) {
     const uint64_t who = __ballot(in && key >= lim);
+    if (!who) return;
     if (who >> (threadIdx.x & 63) & 1) c->at[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0))] = key;
     n += __popcll(who);
+    sorted = false;
   }
-  // one key a lane (0: none) of what will be offered: their k-th greatest bounds what is looked for
-  __device__ __forceinline__ void bound_by(uint64_t key) {
-    c->lane[threadIdx.x & 63] = key;
-    wave_sync();
-    const uint64_t kth = __ballot(key && greater(c->lane, 64, key) == k - 1);
-    wave_sync();
-    if (kth) bound(fpi::readlane_u64(key, __builtin_ctzll(kth)));
+  // One value a lane of what will be offered: at least k of them reach the bound,
+  // which has the upper 16 bits of their k-th greatest.
+  __device__ __forceinline__ void bound_by(float x) {
+    const uint32_t o = ordered(x);
+    uint32_t t = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit)
+      if (__popcll(__ballot(o >= (t | 1u << bit))) >= k) t |= 1u << bit;
+    if (t > ordered(-__FLT_MAX__)) bound((uint64_t)t << 32);
   }
 };
 
-// What a row's statistics and its sorted keys say, written down.
+// What a row's statistics and its sorted keys say, written down by one wave.
 template <typename E>
 __device__ __forceinline__ void finish_row(const LogArgs& a, int64_t t, const Stats& st, const uint64_t* best, int have) {
   const bool bad = st.s != st.s, empty = st.s == 0.f;
@@ -180,11 +196,34 @@ __device__ __forceinline__ void finish_row(const LogArgs& a, int64_t t, const St
     a.max[t] = st.m;
     a.logsum[t] = log_s;
   }
-  if ((int)threadIdx.x < a.top) {
-    const uint64_t k = (int)threadIdx.x < have ? best[threadIdx.x] : 0;
-    const bool none = bad || k == 0 || key_index(k) >= (uint32_t)a.V;
-    a.top_ids[t * a.top + threadIdx.x] = none ? -1 : (int32_t)key_index(k);
-    a.top_lp[t * a.top + threadIdx.x] = bad ? __builtin_nanf("") : (none ? -__builtin_inff() : log_p(key_value(k)));
+  int32_t* const ids = a.top_ids + t * a.top;
+  float* const lps = a.top_lp + t * a.top;
+  const int lane = threadIdx.x;
+  if (lane < a.top) {
+    if (bad) {
+      ids[lane] = -1;
+      lps[lane] = __builtin_nanf("");
+    } else if (lane < have) {
+      ids[lane] = (int32_t)key_index(best[lane]);
+      lps[lane] = log_p(key_value(best[lane]));
+    }
+  }
+  if (bad || have >= a.top) return;
+  // fewer tokens than asked for can come: the first ones that cannot, then none
+  const E* const row = (const E*)a.X + t * a.ldx;
+  for (int64_t i = lane; i - lane < a.V && have < a.top; i += 64) {
+    const bool out = i < a.V && sdev::elem_float(row + i) == -__builtin_inff();
+    const uint64_t who = __ballot(out);
+    const int at = have + (int)__popcll(who & ((1ull << lane) - 1));
+    if (out && at < a.top) {
+      ids[at] = (int32_t)i;
+      lps[at] = -__builtin_inff();
+    }
+    have += (int)__popcll(who);
+  }
+  if (lane >= have && lane < a.top) {
+    ids[lane] = -1;
+    lps[lane] = -__builtin_inff();
   }
 }
 
@@ -257,16 +296,7 @@ __global__ __launch_bounds__(NT, 4) void logprob_kernel(LogArgs a) {
       if (!who) continue;
       anew();
       auto index = [&](int v, int e) { return (uint32_t)(base + (v * NT + tid) * EV + e); };
-      if (__popcll(who) >= a.top) {
-        uint64_t best = 0;
-#pragma unroll
-        for (int v = NV - 1; v >= 0; --v)
-          if (vm[v] == mt)
-#pragma unroll
-            for (int e = EV - 1; e >= 0; --e)
-              if (load_elem<E>(raw[v], e) == mt) best = make_key(mt, index(v, e));
-        top.bound_by(best);
-      }
+      if (__popcll(who) >= a.top) top.bound_by(mt);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (__ballot(vm[v] >= top.least)) {
@@ -277,36 +307,47 @@ __global__ __launch_bounds__(NT, 4) void logprob_kernel(LogArgs a) {
             if (__ballot(x >= top.least)) top.offer(make_key(x, index(v, e)), x >= top.least);
           }
         }
-      if (top.n > a.top) top.sort();
+      if (top.n > 48) top.sort();
     }
     if (a.top) {
       top.sort();
       if (lane == 0) found[wave] = top.n;
     }
     st = block_stats(st, k2, red);
-    if (wave == 0) {
-      if (a.top) {
+    int have = 0;
+    if (a.top) {  // the waves' sorted keys as one list, in the places of the first wave's candidates behind its own
+      uint64_t* const all = keys[0].at + FP_MAX_TOP;
 #pragma unroll
-        for (int w = 1; w < NT / 64; ++w) top.offer(lane < found[w] ? keys[w].at[lane] : 0, lane < found[w]);
-        top.sort();
+      for (int w = 0; w < NT / 64; ++w) have += found[w];
+      if (lane < found[wave]) {
+        const uint64_t mine = keys[wave].at[lane];
+        int rank = lane;
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w) rank += greater_sorted(keys[wave ^ w].at, found[wave ^ w], mine);
+        if (rank < a.top) all[rank] = mine;
       }
+      have = min(have, a.top);
+      __syncthreads();
+    }
+    if (wave == 0) {
+      const uint64_t* const all = keys[0].at + FP_MAX_TOP;
       if (a.splits == 1) {
-        finish_row<E>(a, t, st, keys[0].at, top.n);
+        finish_row<E>(a, t, st, all, have);
       } else {
         if (tid == 0) {
           a.stats[task * 3] = st.m;
           a.stats[task * 3 + 1] = st.s;
           a.stats[task * 3 + 2] = st.u;
         }
-        if (tid < a.top) a.keys[task * a.top + tid] = tid < top.n ? keys[0].at[tid] : 0;
+        if (tid < a.top) a.keys[task * a.top + tid] = tid < have ? all[tid] : 0;
       }
     }
     __syncthreads();  // the next row's candidates take the place of these
   }
 }
 
-// A row's parts joined, a wave to a row. The parts' keys are sorted: the k-th
-// greatest of their first ones bounds what is looked for.
+// A row's parts joined, a wave to a row. The parts' keys are sorted: their first
+// ones bound what is looked for.
 template <typename E>
 __global__ __launch_bounds__(64) void logprob_join_kernel(LogArgs a) {
   __shared__ Keys keys;
@@ -325,7 +366,10 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(LogArgs a) {
       uint64_t key[PARTS * FP_MAX_TOP / 64];
 #pragma unroll
       for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) key[i] = lane + 64 * i < n ? from[lane + 64 * i] : 0;
-      if (a.splits >= a.top) top.bound_by(lane < a.splits ? from[lane * a.top] : 0);
+      if (a.splits >= a.top) {
+        const uint64_t first = lane < a.splits ? from[lane * a.top] : 0;
+        top.bound_by(first ? key_value(first) : -__builtin_inff());
+      }
 #pragma unroll
       for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) {
         top.room(64);
