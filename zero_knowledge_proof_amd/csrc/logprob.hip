@@ -346,8 +346,8 @@ __global__ __launch_bounds__(NT, 4) void logprob_kernel(LogArgs a) {
   }
 }
 
-// A row's parts joined, a wave to a row. The parts' keys are sorted: their first
-// ones bound what is looked for.
+// A row's parts joined, a wave to a row. The parts' keys are sorted: the first ones
+// of each, 64 in all, bound what is looked for.
 template <typename E>
 __global__ __launch_bounds__(64) void logprob_join_kernel(LogArgs a) {
   __shared__ Keys keys;
@@ -366,10 +366,9 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(LogArgs a) {
       uint64_t key[PARTS * FP_MAX_TOP / 64];
 #pragma unroll
       for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) key[i] = lane + 64 * i < n ? from[lane + 64 * i] : 0;
-      if (a.splits >= a.top) {
-        const uint64_t first = lane < a.splits ? from[lane * a.top] : 0;
-        top.bound_by(first ? key_value(first) : -__builtin_inff());
-      }
+      const int j = lane / a.splits;
+      const uint64_t ahead = j < 64 / a.splits && j < a.top ? from[(lane % a.splits) * a.top + j] : 0;
+      top.bound_by(ahead ? key_value(ahead) : -__builtin_inff());
 #pragma unroll
       for (int i = 0; i < PARTS * FP_MAX_TOP / 64; ++i) {
         top.room(64);
@@ -455,19 +454,26 @@ int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == F
 struct Plan {
   int nv, splits, per;
 };
-// Rows that fill the GPU are not cut; fewer are, into up to 32 parts.
+// Cuts rows into the parts that take the least rounds of the 1024 workgroups that
+// the GPU holds, a part costing a chunk more than it has.
 Plan plan_rows(fp_dtype dt, int32_t T, int32_t V) {
   const int64_t ev = 16 / elem_bytes(dt);
   auto chunks = [&](int nv) { return ((int64_t)V + NT * nv * ev - 1) / (NT * nv * ev); };
-  Plan p{8, 1, 1};
-  if (V <= NT * 2 * ev || T * chunks(8) < 512) p.nv = 2;
+  // four vectors a thread, two where that leaves too few chunks for the GPU (2048
+  // rows of 131072 bf16 with 20 top tokens 135 us, two 144, eight 140; 333 rows of
+  // 50001 fp32 with 5: two 25.5, eight 30)
+  Plan p{4, 1, 1};
+  if (V <= NT * 2 * ev || T * chunks(8) < 4096) p.nv = 2;
   const int64_t c = chunks(p.nv);
   if (c == 0 || T == 0) return p;
-  int64_t s = (1024 + T - 1) / T;
-  s = s < c ? s : c;
-  s = s < PARTS ? s : PARTS;
-  p.per = (int)((c + s - 1) / s);
-  p.splits = (int)((c + p.per - 1) / p.per);
+  int64_t least = INT64_MAX;
+  for (int64_t s = 1; s <= PARTS && s <= c; ++s) {
+    const int64_t per = (c + s - 1) / s, cost = ((T * s + 1023) / 1024) * (per + 1);
+    if (cost >= least) continue;
+    least = cost;
+    p.per = (int)per;
+    p.splits = (int)((c + per - 1) / per);
+  }
   return p;
 }
 
@@ -490,7 +496,7 @@ template <typename E>
 int launch_rows(const LogArgs& a, int nv, hipStream_t st) {
   const int64_t tasks = (int64_t)a.T * a.splits;
   const dim3 grid((unsigned)(tasks < (1 << 20) ? tasks : 1 << 20));
-  if (nv == 8) logprob_kernel<E, 8><<<grid, dim3(NT), 0, st>>>(a);
+  if (nv == 4) logprob_kernel<E, 4><<<grid, dim3(NT), 0, st>>>(a);
   else logprob_kernel<E, 2><<<grid, dim3(NT), 0, st>>>(a);
   int rc = fpi::check_launch("logprob_kernel");
   if (rc || a.splits == 1) return rc;
