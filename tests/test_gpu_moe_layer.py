@@ -92,7 +92,8 @@ def route(g, T, K, E, drop=0.0, wide=False):
 # one token to as many slots as there are; one expert to more than a word of the bitmap; ragged widths around every tile and unit
 CASES = [(1, 1, 1, 64, 64), (1, 8, 128, 256, 128), (2, 2, 4, 1, 1), (3, 2, 5, 15, 17), (8, 2, 16, 512, 768), (5, 4, 33, 63, 31),
          (9, 1, 3, 65, 33), (16, 2, 4, 100, 257), (33, 1, 1, 128, 96), (61, 3, 20, 200, 333), (64, 16, 40, 48, 64), (64, 1, 2, 1000, 130),
-         (1, 16, 600, 40, 40), (7, 3, 1024, 24, 40), (1024, 1, 12, 32, 64), (10, 100, 7, 64, 32), (4, 2, 6, 2100, 1029), (12, 5, 9, 129, 2050)]
+         (1, 16, 600, 40, 40), (7, 3, 1024, 24, 40), (1024, 1, 12, 32, 64), (10, 100, 7, 64, 32), (4, 2, 6, 2100, 1029), (12, 5, 9, 129, 2050), (2, 1, 3, 64, 5000), (8, 8, 64, 640, 2100),
+         (20, 1, 3, 64, 5000), (40, 2, 60, 640, 1100)]
 
 
 @pytest.mark.parametrize("T,K,E,d,ff", CASES)
@@ -237,6 +238,31 @@ def test_table_of_experts(fp):
     W = torch.randint(-8, 8, (5, 40, 70), device="cuda", dtype=torch.int8)
     P = fp.pack_experts(W)
     assert P.table.tolist() == [w.data.data_ptr() for w in P.weights] == [ctypes.c_void_p(p).value for p in P.ptrs]
+
+
+def test_experts_put_together_inside_a_capture(fp):
+    """The packed weights as experts again, inside a capture: the grouped product's launch needs no table, the layer's refuses
+    there, and has it afterwards."""
+    g = torch.Generator("cuda").manual_seed(13)
+    L = Layer(fp, g, 3, 64, 96, False)
+    X = tokens(g, 5, 64, torch.bfloat16)
+    q, s = fp.quantize_rows(X)
+    ids, w = route(g, 5, 2, 3)
+    plan = fp.moe_sort(ids, 3)
+    want, layer = fp.scaled_matmul_grouped(q, s, L.P["up"], L.s["up"], plan.offsets, rows=plan.tokens), L(fp, X, ids, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        up = fp.PackedExperts(L.P["up"].weights)
+        Y = fp.scaled_matmul_grouped(q, s, up, L.s["up"], plan.offsets, rows=plan.tokens)
+        with pytest.raises(ValueError, match="capture"):
+            fp.moe_layer(X, ids, w, up, L.s["up"], L.P["down"], L.s["down"])
+    for _ in range(2):
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
+    assert torch.equal(fp.moe_layer(X, ids, w, up, L.s["up"], L.P["down"], L.s["down"]), layer)
 
 
 class _Norm(torch.autograd.Function):

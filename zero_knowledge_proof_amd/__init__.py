@@ -889,11 +889,24 @@ class PackedExperts:
         # (first expert, how many, their addresses in ptrs): a launch takes MAX_GROUPS
         counts = [(g, min(MAX_GROUPS, len(weights) - g)) for g in range(0, len(weights), MAX_GROUPS)]
         self.parts = [(g, n, (ctypes.c_void_p * n).from_buffer(self.ptrs, g * ctypes.sizeof(ctypes.c_void_p))) for g, n in counts]
-        # the addresses on the device, for calls whose experts only the device knows
-        self.table = torch.tensor([w.data.data_ptr() for w in weights], dtype=torch.int64).to(self.device)
+        self._table = None
+        if not self._capturing():
+            self.table  # now, so that a call may be captured
 
     def __len__(self):
         return len(self.weights)
+
+    def _capturing(self) -> bool:
+        return self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+    @property
+    def table(self):
+        """The weights' addresses on the device (int64 [G]), for calls whose experts only the device knows."""
+        if self._table is None:
+            if self._capturing():
+                raise ValueError("experts packed inside a capture: their addresses reach the device only outside of one")
+            self._table = torch.tensor([w.data.data_ptr() for w in self.weights], dtype=torch.int64).to(self.device)
+        return self._table
 
 
 def pack_experts(W) -> PackedExperts:

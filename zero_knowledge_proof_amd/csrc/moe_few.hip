@@ -57,15 +57,15 @@ struct FewArgs {
   int64_t ldws[2];
   int32_t d_in, d_out;         // of this launch's products
   int32_t nb;                  // K blocks
+  int32_t d;                   // of the layer's output
   int32_t panels;              // of 32 outputs
   float* A;                    // [slots][lda]: ff values, then whole pieces
   int64_t lda;
   float* top;                  // [slots][ldt]: largest magnitude of each panel of ff, then zeros to whole pieces
   int32_t ldt;
-  int32_t* zero;               // count and part, which the first launch clears
-  int64_t n_zero;
-  uint32_t* count;             // arrivals at each 32 outputs, in units
-  int32_t* part;               // [slots][d]: the products of a_s and D
+  uint32_t* count;             // arrivals at each 32 outputs, in units; cleared by the first launch,
+  int32_t* part;               // [slots][d]: the products of a_s and D; cleared where they are added up
+  int32_t out_panels, out_units, out_grid;  // of the second launch: panels, units of each, workgroups
   float* xs_out;               // [slots][panels]: the scales of the rows a_s
   const float* weights;        // [T][K]
   void* Y;
@@ -383,16 +383,29 @@ __device__ __forceinline__ void experts_of(const FewArgs& a, int64_t first, int6
   }
 }
 
+// In the second launch, whole panels for every workgroup, or parts of panels where
+// whole ones would leave many workgroups idle and the parts are worth their
+// additions: with fewer panels than CUs, or with a last round that few workgroups
+// have (8 tokens of 2 of 16 experts, 14336 -> 4096: 110 us, uncut 140; 61 tokens of 3
+// of 20, 2003 -> 1000, cut 38 us, uncut 24).
+__device__ __forceinline__ bool cut_panels(const FewArgs& a, int present) {
+  const int64_t panels = (int64_t)present * a.out_panels, rounds = (panels + a.out_grid - 1) / a.out_grid;
+  return a.out_units >= 2 * NW && (panels < CUS || (rounds > 1 && panels * 10 < rounds * a.out_grid * 9));
+}
+
 template <int MAPS, typename XT, bool WHOLE>
 __global__ __launch_bounds__(NT, WGS) void moe_hidden_kernel(FewArgs a) {
   using L = Lds<MAPS, XT>;
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
   const int tid = threadIdx.x;
-  // what the outputs' launch counts and adds up from zero
-  for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < a.n_zero; i += (int64_t)gridDim.x * NT) a.zero[i] = 0;
   const int present = find_experts(a.ids, lds), NU = (a.nb + Unit<MAPS, ROWS>::BLOCKS - 1) / Unit<MAPS, ROWS>::BLOCKS;
   if (present == 0) return;
+  for (int i = blockIdx.x * NT + tid; i < a.out_panels; i += gridDim.x * NT) a.count[i] = 0;
+  if (cut_panels(a, present)) {
+    const int64_t n = (int64_t)a.ids.T * a.ids.K * a.d;
+    for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < n; i += (int64_t)gridDim.x * NT) a.part[i] = 0;
+  }
   const int64_t panels = (int64_t)present * a.panels;
   const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, panels);
   experts_of(a, share(panels, b, wgs) * NU, share(panels, b + 1, wgs) * NU, (int64_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
@@ -455,18 +468,14 @@ __global__ __launch_bounds__(NT, WGS) void moe_output_kernel(FewArgs a) {
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
   const int tid = threadIdx.x;
-  const int present = find_experts(a.ids, lds), NU = (a.nb + Unit<1, ROWS>::BLOCKS - 1) / Unit<1, ROWS>::BLOCKS;
+  const int present = find_experts(a.ids, lds), NU = a.out_units;
   if (present == 0) {  // no token has an expert
     for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < (int64_t)a.ids.T * a.d_out; i += (int64_t)gridDim.x * NT)
       store_out(a, (int)(i / a.d_out), (int)(i % a.d_out), 0.f);
     return;
   }
-  // Whole panels for every workgroup, or parts of panels where whole ones would
-  // leave many workgroups idle and the parts are worth their additions: with fewer
-  // panels than CUs, or with a last round that few workgroups have.
   const int64_t panels = (int64_t)present * a.panels, all = panels * NU;
-  const int64_t rounds = (panels + gridDim.x - 1) / gridDim.x;
-  const bool cut = NU >= 2 * NW && (panels < CUS || (rounds > 1 && panels * 10 < rounds * gridDim.x * 9));
+  const bool cut = cut_panels(a, present);
   const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, cut ? all / (2 * NW) : panels);
   const int64_t first = cut ? share(all, b, wgs) : share(panels, b, wgs) * NU;
   const int64_t end = cut ? share(all, b + 1, wgs) : share(panels, b + 1, wgs) * NU;
@@ -569,7 +578,8 @@ Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
   Scratch s{};
   size_t at = 0;
   auto take = [&](int64_t bytes) { const size_t p = at; at += fpi::align_up((size_t)bytes, 256); return p; };
-  s.part = take(((d + 31) / 32 + N * d) * 4);  // behind the arrivals
+  take((d + 31) / 32 * 4);  // arrivals
+  s.part = take(N * d * 4);
   s.A = take(N * chunked(ff) * 4);
   s.xs_out = take(N * ((d + 31) / 32) * 4);
   if (T <= FEW) {
@@ -612,9 +622,8 @@ void launch_hidden(int x_dt, const FewArgs& a, int64_t most, bool whole, hipStre
   else launch_hidden_rows<MAPS, __hip_bfloat16>(a, most, whole, st);
 }
 template <typename XT>
-void launch_output(const FewArgs& a, int64_t most, hipStream_t st) {
-  const int64_t units = (a.nb + Unit<1, rows_of<XT>()>::BLOCKS - 1) / Unit<1, rows_of<XT>()>::BLOCKS;
-  moe_output_kernel<XT><<<few_grid(most * a.panels * units), dim3(NT), 0, st>>>(a);
+void launch_output(const FewArgs& a, hipStream_t st) {
+  moe_output_kernel<XT><<<dim3((unsigned)a.out_grid), dim3(NT), 0, st>>>(a);
 }
 
 }  // namespace
@@ -664,8 +673,13 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   const int64_t most = T * K < E ? T * K : E;  // experts that the tokens can meet
   FewArgs h{};
   h.ids = Ids{ids, id_bytes == 8, T, K, E};
-  h.zero = (int32_t*)(w + s.part);
-  h.n_zero = (d + 31) / 32 + (int64_t)T * K * d;
+  h.count = (uint32_t*)w;
+  h.part = (int32_t*)(w + s.part);
+  h.d = d;
+  const int blocks = few ? Unit<1, rows_of<float>()>::BLOCKS : Unit<1, rows_of<int8_t>()>::BLOCKS;
+  h.out_panels = (d + 31) / 32;
+  h.out_units = ((ff + WP_BK - 1) / WP_BK + blocks - 1) / blocks;
+  h.out_grid = (int32_t)few_grid(most * h.out_panels * h.out_units).x;
   h.A = (float*)(w + s.A);
   h.lda = chunked(ff);
   h.top = few ? (float*)(w + s.top) : nullptr;
@@ -696,22 +710,20 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   o.d_in = ff;
   o.d_out = d;
   o.nb = (ff + WP_BK - 1) / WP_BK;
-  o.panels = (d + 31) / 32;
-  o.count = (uint32_t*)o.zero;
-  o.part = o.zero + o.panels;
+  o.panels = o.out_panels;
   o.xs_out = (float*)(w + s.xs_out);
   o.weights = weights;
   o.Y = Y;
   o.ldy = ldy;
   o.y_dt = y_dt;
   if (few) {
-    launch_output<float>(o, most, stream);
+    launch_output<float>(o, stream);
   } else {
     r = fp_quantize_rows(FP_F32, o.A, o.lda, T * K, ff, (int8_t*)(w + s.aq), o.lda, (float*)(w + s.as), stream);
     if (r) return r;
     o.X = w + s.aq;
     o.xs = (const float*)(w + s.as);
-    launch_output<int8_t>(o, most, stream);
+    launch_output<int8_t>(o, stream);
   }
   r = fpi::check_launch("moe_output_kernel");
   return r ? r : fpi::ok();
