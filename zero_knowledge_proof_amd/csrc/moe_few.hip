@@ -50,7 +50,7 @@ struct Ids {
 struct FewArgs {
   Ids ids;
   const void* X;  // [T] tokens' rows (first launch)
-  int64_t ldx;
+  int64_t ldx, x_bytes;        // x_bytes: from the first row's start to the last one's end
   const float* xs;             // of int8 rows
   const int8_t* const* W[2];   // the experts' packed weights: up and gate, or down
   const float* ws[2];          // their scales
@@ -79,8 +79,8 @@ constexpr int NW = 4, NT = NW * 64;  // waves, each with units of K in turn
 constexpr int WGS = 3;               // workgroups that a CU holds
 constexpr int CUS = 256;
 
-// A unit of K: the blocks of it that a wave takes together, 8 KiB of weights (4
-// for 32 rows and one matrix, for the sake of LDS).
+// A unit of K: the blocks of it that a wave takes together (two for 32 rows, for the
+// sake of LDS).
 template <int MAPS, int ROWS>
 struct Unit {
   static constexpr int BLOCKS = ROWS == 8 ? 4 / MAPS : 2, K = BLOCKS * WP_BK, PIECES = K / 128, XP = K + 16;
@@ -102,14 +102,27 @@ struct Lds {
 constexpr int NONE = 0xFFFF;
 static_assert(FP_MAX_EXPERTS < NONE && SLOTS <= NONE, "experts and slots in 16 bits");
 
-// The slots' experts and the list of those met. Returns how many are met.
-template <typename L>
-__device__ __forceinline__ int find_experts(const Ids& ids, L& lds) {
+// One 64-byte line a thread of `bytes` at p, another 16 KiB for every eighth
+// workgroup (one of each XCD), on its way to the XCD's L2 while the experts are
+// found: what is read behind the ids comes from memory otherwise, one after another.
+// `kept` keeps the loads.
+__device__ __forceinline__ int early(const void* p, int64_t bytes) {
+  const int64_t at = ((int64_t)(blockIdx.x / 8) * NT + threadIdx.x) * 64;
+  return at + 4 <= bytes ? *(const int*)(((uintptr_t)p & ~(uintptr_t)3) + at) : 0;
+}
+__device__ __forceinline__ void kept(int x) { asm volatile("" : : "v"(x)); }
+
+// The slots' experts and the list of those met. Returns how many are met. What
+// ahead() loads goes behind the ids.
+template <typename L, typename Ahead>
+__device__ __forceinline__ int find_experts(const Ids& ids, L& lds, Ahead ahead) {
   const int tid = threadIdx.x, N = ids.T * ids.K, words = (ids.E + 31) / 32;
+  const int mine = tid < N ? ids.at(tid) : -1;
+  ahead();
   for (int i = tid; i < words; i += NT) lds.bits[i] = 0;
   __syncthreads();
   for (int i = tid; i < N; i += NT) {
-    const int e = ids.at(i);
+    const int e = i == tid ? mine : ids.at(i);
     lds.id[i] = (uint16_t)e;  // NONE for -1
     if (e >= 0) atomicOr(&lds.bits[e >> 5], 1u << (e & 31));
   }
@@ -253,8 +266,10 @@ struct Piece {
 };
 
 // A range of units, [from, to) of a stream in which panel t has [t NU, (t + 1) NU).
+// All of a launch's units are at most FP_MAX_EXPERTS * 2^12 * 2^9 = 2^31. (Divisions
+// in 64 bits took 1 us of a workgroup's 10.)
 struct Range {
-  int64_t from, to;
+  uint32_t from, to;
 };
 
 // The products of nr rows (at most ROWS; row(i) their addresses) with a range of
@@ -302,8 +317,8 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
   };
   int8_t* xs = lds.x[wave] + (lane >> 3) * U::XP + kc;
   const int8_t* xf = lds.x[wave] + (r & (ROWS - 1)) * U::XP + 32 * h;  // fragments
-  const int t0 = (int)(range.from / NU), t1 = (int)((range.to + NU - 1) / NU);
-  const int first = (int)(range.from - (int64_t)t0 * NU), last = (int)(range.to - (int64_t)(t1 - 1) * NU);
+  const int t0 = (int)(range.from / (uint32_t)NU), t1 = (int)((range.to - 1) / (uint32_t)NU) + 1;
+  const int first = (int)(range.from - (uint32_t)t0 * NU), last = (int)(range.to - (uint32_t)(t1 - 1) * NU);
   auto start = [&](int t) { return (t == t0 ? first : 0) + wave; };
   auto limit = [&](int t) { return t == t1 - 1 ? last : NU; };
   // the wave's first unit of panel t or, where it has none there, of a later one
@@ -368,14 +383,17 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
 }
 
 // Where the share of `all` of workgroup b of n begins.
-__device__ __forceinline__ int64_t share(int64_t all, int b, int n) { return all * min(b, n) / n; }
+__device__ __forceinline__ uint32_t share(uint32_t all, uint32_t b, uint32_t n) {
+  const uint32_t q = all / n, rest = all - q * n;
+  return b < n ? b * q + min(b, rest) : all;
+}
 
 // The experts' parts of the stream's range [first, end), with `all` units each, in
 // turn: part(expert, range within it, its number of slots).
 template <typename L, typename Part>
-__device__ __forceinline__ void experts_of(const FewArgs& a, int64_t first, int64_t end, int64_t all, L& lds, Part part) {
-  for (int64_t at = first; at < end;) {
-    const int j = (int)(at / all);
+__device__ __forceinline__ void experts_of(const FewArgs& a, uint32_t first, uint32_t end, uint32_t all, L& lds, Part part) {
+  for (uint32_t at = first; at < end;) {
+    const uint32_t j = at / all;
     const Range range{at - j * all, min(all, end - j * all)};
     at += range.to - range.from;
     const int e = __builtin_amdgcn_readfirstlane(lds.met[j]);
@@ -389,8 +407,8 @@ __device__ __forceinline__ void experts_of(const FewArgs& a, int64_t first, int6
 // have (8 tokens of 2 of 16 experts, 14336 -> 4096: 110 us, uncut 140; 61 tokens of 3
 // of 20, 2003 -> 1000, cut 38 us, uncut 24).
 __device__ __forceinline__ bool cut_panels(const FewArgs& a, int present) {
-  const int64_t panels = (int64_t)present * a.out_panels, rounds = (panels + a.out_grid - 1) / a.out_grid;
-  return a.out_units >= 2 * NW && (panels < CUS || (rounds > 1 && panels * 10 < rounds * a.out_grid * 9));
+  const uint32_t panels = (uint32_t)present * a.out_panels, rounds = (panels + a.out_grid - 1) / a.out_grid;
+  return a.out_units >= 2 * NW && (panels < CUS || (rounds > 1 && (uint64_t)panels * 10 < (uint64_t)rounds * a.out_grid * 9));
 }
 
 template <int MAPS, typename XT, bool WHOLE>
@@ -399,16 +417,22 @@ __global__ __launch_bounds__(NT, WGS) void moe_hidden_kernel(FewArgs a) {
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
   const int tid = threadIdx.x;
-  const int present = find_experts(a.ids, lds), NU = (a.nb + Unit<MAPS, ROWS>::BLOCKS - 1) / Unit<MAPS, ROWS>::BLOCKS;
+  int soon[1 + MAPS];
+  const int present = find_experts(a.ids, lds, [&]() {
+    soon[0] = early(a.X, a.x_bytes);
+#pragma unroll
+    for (int i = 0; i < MAPS; ++i) soon[1 + i] = early(a.W[i], (int64_t)a.ids.E * 8);
+  });
+  const int NU = (a.nb + Unit<MAPS, ROWS>::BLOCKS - 1) / Unit<MAPS, ROWS>::BLOCKS;
   if (present == 0) return;
   for (int i = blockIdx.x * NT + tid; i < a.out_panels; i += gridDim.x * NT) a.count[i] = 0;
   if (cut_panels(a, present)) {
     const int64_t n = (int64_t)a.ids.T * a.ids.K * a.d;
     for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < n; i += (int64_t)gridDim.x * NT) a.part[i] = 0;
   }
-  const int64_t panels = (int64_t)present * a.panels;
-  const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, panels);
-  experts_of(a, share(panels, b, wgs) * NU, share(panels, b + 1, wgs) * NU, (int64_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
+  const uint32_t panels = (uint32_t)present * a.panels;
+  const uint32_t b = blockIdx.x, wgs = min(gridDim.x, panels);
+  experts_of(a, share(panels, b, wgs) * NU, share(panels, b + 1, wgs) * NU, (uint32_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
     Weights W[MAPS];
 #pragma unroll
     for (int i = 0; i < MAPS; ++i) W[i] = (Weights)a.W[i][e];
@@ -451,6 +475,8 @@ __global__ __launch_bounds__(NT, WGS) void moe_hidden_kernel(FewArgs a) {
       });
     }
   });
+#pragma unroll
+  for (int i = 0; i < 1 + MAPS; ++i) kept(soon[i]);
 }
 
 __device__ __forceinline__ void store_out(const FewArgs& a, int t, int o, float f) {
@@ -468,19 +494,25 @@ __global__ __launch_bounds__(NT, WGS) void moe_output_kernel(FewArgs a) {
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
   const int tid = threadIdx.x;
-  const int present = find_experts(a.ids, lds), NU = a.out_units;
+  int soon[3];
+  const int present = find_experts(a.ids, lds, [&]() {
+    soon[0] = early(a.W[0], (int64_t)a.ids.E * 8);
+    soon[1] = sizeof(XT) > 1 ? early(a.top, (int64_t)a.ids.T * a.ids.K * a.ldt * 4) : 0;
+    soon[2] = early(a.X, a.x_bytes);
+  });
+  const int NU = a.out_units;
   if (present == 0) {  // no token has an expert
     for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < (int64_t)a.ids.T * a.d_out; i += (int64_t)gridDim.x * NT)
       store_out(a, (int)(i / a.d_out), (int)(i % a.d_out), 0.f);
     return;
   }
-  const int64_t panels = (int64_t)present * a.panels, all = panels * NU;
+  const uint32_t panels = (uint32_t)present * a.panels, all = panels * NU;
   const bool cut = cut_panels(a, present);
-  const int b = blockIdx.x, wgs = (int)min((int64_t)gridDim.x, cut ? all / (2 * NW) : panels);
-  const int64_t first = cut ? share(all, b, wgs) : share(panels, b, wgs) * NU;
-  const int64_t end = cut ? share(all, b + 1, wgs) : share(panels, b + 1, wgs) * NU;
+  const uint32_t b = blockIdx.x, wgs = min(gridDim.x, cut ? all / (2 * NW) : panels);
+  const uint32_t first = cut ? share(all, b, wgs) : share(panels, b, wgs) * NU;
+  const uint32_t end = cut ? share(all, b + 1, wgs) : share(panels, b + 1, wgs) * NU;
   if (first == end) return;
-  experts_of(a, first, end, (int64_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
+  experts_of(a, first, end, (uint32_t)a.panels * NU, lds, [&](int e, const Range& range, int n) {
     const Weights W[1] = {(Weights)a.W[0][e]};
     for (int r0 = 0; r0 < n; r0 += ROWS) {
       const int nr = min(n - r0, ROWS);
@@ -518,19 +550,21 @@ __global__ __launch_bounds__(NT, WGS) void moe_output_kernel(FewArgs a) {
       });
     }
   });
+#pragma unroll
+  for (int i = 0; i < 3; ++i) kept(soon[i]);
   // each thread's additions are at the agent's level before its workgroup's arrivals count
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_s_waitcnt(0);
   const uint32_t units = (uint32_t)present * NU;  // of 32 outputs, in all experts
-  const int64_t p0 = first / NU, p1 = (end + NU - 1) / NU;
-  for (int64_t base = p0; base < p1; base += NT) {
+  const uint32_t p0 = first / (uint32_t)NU, p1 = (end - 1) / (uint32_t)NU + 1;
+  for (uint32_t base = p0; base < p1; base += NT) {
     __syncthreads();
     if (tid == 0) lds.last = 0;
     __syncthreads();
-    const int64_t p = base + tid;
+    const uint32_t p = base + tid;
     if (p < p1) {
-      const int t = (int)(p % a.panels);
-      const uint32_t mine = (uint32_t)(min(end, (p + 1) * NU) - max(first, p * NU));
+      const int t = (int)(p % (uint32_t)a.panels);
+      const uint32_t mine = min(end - p * NU, (uint32_t)NU) - (p == p0 ? first - p0 * NU : 0);
       if (__hip_atomic_fetch_add(&a.count[t], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine == units)
         lds.tile[atomicAdd(&lds.last, 1)] = (uint16_t)t;
     }
@@ -688,6 +722,7 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   FewArgs o = h;
   h.X = X;
   h.ldx = ldx;
+  h.x_bytes = ((T - 1) * ldx + d) * (x_dt == FP_I8 ? 1 : elem_bytes(x_dt));
   h.xs = x_scale;
   h.W[0] = up;
   h.ws[0] = up_scale;
@@ -704,6 +739,7 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   if (r) return r;
   o.X = o.A;
   o.ldx = o.lda;
+  o.x_bytes = (int64_t)T * K * o.lda * (few ? 4 : 1);
   o.W[0] = down;
   o.ws[0] = down_scale;
   o.ldws[0] = ld_down;
