@@ -203,8 +203,8 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
                             const int32_t* rows, const float* w, int32_t T, int32_t K, int32_t d, void* dO,
                             int64_t lddo, float* dw, hipStream_t stream);
 
-/* A mixture-of-experts layer for a few tokens in two launches, with the
- * products, the row quantization and the sums of the calls it stands for
+/* A mixture-of-experts layer for a few tokens in two launches (four for more
+ * than 8 tokens whose rows are floats, three for int8 ones), with the products, the row quantization and the sums of the calls it stands for
  * (fp_scaled_linear by expert, twice, and fp_moe_combine):
  *   a[t, k] = silu(G x_t) * (U x_t)  (gate NULL: silu(U x_t)), fp32;
  *             silu(v) = v / (1 + exp(-v)); G, U the weights of expert ids[t, k]

@@ -777,31 +777,41 @@ def scaled_linear(X, Wp: PackedWeights, w_scale, bias=None, out=None, dtype=None
 
 
 # ------------------------------------------------------------------- norms --
+def _rows_like(t, dtype, shape, name: str) -> int:
+    """_matrix of a given type and shape, at once where its rows are as they mostly are."""
+    if t.dtype is dtype and t.shape == shape:
+        ld, one = t.stride()
+        if one == 1 and ld >= shape[1]:
+            return ld
+    return _matrix(t, dtype, shape[0], shape[1], name)
+
+
 def _norm_args(X, weight, name: str):
-    """Rows' type and width, the weights' type and address."""
-    if X.dim() != 2:
-        raise ValueError("%s: shape %s, expected two dimensions" % (name, tuple(X.shape)))
-    T, d = X.shape
-    dt = _float_dt(X.dtype, name)
+    """Rows' shape, type, the library's name for it, leading dimension, the weights' type and address."""
+    shape, dtype = X.shape, X.dtype
+    if len(shape) != 2:
+        raise ValueError("%s: shape %s, expected two dimensions" % (name, tuple(shape)))
+    dt = _float_dt(dtype, name)
+    ld = _rows_like(X, dtype, shape, name)
     if weight is None:
-        return T, d, dt, dt, 0
-    if weight.dtype is not X.dtype and weight.dtype is not torch.float32:
-        raise ValueError("weight: %s, expected %s or float32" % (weight.dtype, X.dtype))
-    _vector(weight, weight.dtype, (d,), "weight")
-    return T, d, dt, _FLOATS[weight.dtype], weight.data_ptr()
+        return shape, dtype, dt, ld, dt, 0
+    wt = weight.dtype
+    if wt is not dtype and wt is not torch.float32:
+        raise ValueError("weight: %s, expected %s or float32" % (wt, dtype))
+    _vector(weight, wt, shape[1:], "weight")
+    return shape, dtype, dt, ld, _FLOATS[wt], weight.data_ptr()
 
 
-def _stream_rows(X, residual, residual_out):
+def _stream_rows(X, shape, dtype, residual, residual_out):
     """The residual's address and leading dimension, and where the sum goes (made if None and there is a residual)."""
-    T, d = X.shape
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out: no residual to add")
-        return 0, d, None, 0, d
-    ldr = _matrix(residual, X.dtype, T, d, "residual")
+        return 0, shape[1], None, 0, shape[1]
+    ldr = _rows_like(residual, dtype, shape, "residual")
     if residual_out is None:
-        residual_out = torch.empty((T, d), dtype=X.dtype, device=X.device)
-    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), _matrix(residual_out, X.dtype, T, d, "residual_out")
+        residual_out = torch.empty(shape, dtype=dtype, device=X.device)
+    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), _rows_like(residual_out, dtype, shape, "residual_out")
 
 
 def rms_norm(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None):
@@ -811,12 +821,12 @@ def rms_norm(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out
     Sums in fp32. The gradient is rms_norm_backward; no graph is recorded, and tensors that require a gradient are refused
     unless under torch.no_grad."""
     _no_graph("rms_norm_backward", X, weight, residual)
-    T, d, dt, w_dt, w = _norm_args(X, weight, "X")
-    ldx = _matrix(X, None, T, d, "X")
-    r, ldr, H, h, ldh = _stream_rows(X, residual, residual_out)
+    shape, dtype, dt, ldx, w_dt, w = _norm_args(X, weight, "X")
+    T, d = shape
+    r, ldr, H, h, ldh = _stream_rows(X, shape, dtype, residual, residual_out)
     if out is None:
-        out = torch.empty((T, d), dtype=X.dtype, device=X.device)
-    ldy = _matrix(out, X.dtype, T, d, "out")
+        out = torch.empty(shape, dtype=dtype, device=X.device)
+    ldy = _rows_like(out, dtype, shape, "out")
     st = _here(X, weight, residual, H, out)
     _check(lib().fp_rms_norm(dt, X.data_ptr(), ldx, r, ldr, w_dt, w, eps, T, d, h, ldh, out.data_ptr(), ldy, 0, d, 0, st),
            "fp_rms_norm")
@@ -827,19 +837,19 @@ def rms_norm_quantize(X, weight, eps: float = 1e-5, residual=None, residual_out=
     """(Xq, scale), with a ``residual`` (Xq, scale, H): quantize_rows of rms_norm's fp32 rows, for scaled_matmul or
     moe_layer. ``Y`` (X's type) also receives the rows themselves, which a router reads. The int8 rows have no gradient."""
     _no_graph("rms_norm_backward", X, weight, residual)
-    T, d, dt, w_dt, w = _norm_args(X, weight, "X")
-    ldx = _matrix(X, None, T, d, "X")
-    r, ldr, H, h, ldh = _stream_rows(X, residual, residual_out)
+    shape, dtype, dt, ldx, w_dt, w = _norm_args(X, weight, "X")
+    T, d = shape
+    r, ldr, H, h, ldh = _stream_rows(X, shape, dtype, residual, residual_out)
     if out is None:
         out = torch.empty((T, (d + 15) // 16 * 16), dtype=torch.int8, device=X.device)
         if d % 16:
             out = out[:, :d]
-    ldq = _matrix(out, torch.int8, T, d, "out")
+    ldq = _rows_like(out, torch.int8, shape, "out")
     if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=X.device)
     else:
-        _vector(scale, torch.float32, (T,), "scale")
-    y, ldy = (0, d) if Y is None else (Y.data_ptr(), _matrix(Y, X.dtype, T, d, "Y"))
+        _vector(scale, torch.float32, shape[:1], "scale")
+    y, ldy = (0, d) if Y is None else (Y.data_ptr(), _rows_like(Y, dtype, shape, "Y"))
     st = _here(X, weight, residual, H, out, scale, Y)
     _check(lib().fp_rms_norm(dt, X.data_ptr(), ldx, r, ldr, w_dt, w, eps, T, d, h, ldh, y, ldy, out.data_ptr(), ldq,
                              scale.data_ptr(), st), "fp_rms_norm")
@@ -850,12 +860,13 @@ def rms_norm_backward(dY, H, weight, eps: float = 1e-5, dH=None, out=None, dw=No
     """(dX, dw), the gradients of rms_norm at H [T, d] (its X, or the sum it returned) from dY: dX [T, d] in H's type, of X
     and of the residual alike, with ``dH``, the gradient of H's other uses, added; dw float32 [d] (None without weights).
     d is at most 16384."""
-    T, d, dt, w_dt, w = _norm_args(H, weight, "H")
-    ldh, lddy = _matrix(H, None, T, d, "H"), _matrix(dY, H.dtype, T, d, "dY")
-    lddh = d if dH is None else _matrix(dH, H.dtype, T, d, "dH")
+    shape, dtype, dt, ldh, w_dt, w = _norm_args(H, weight, "H")
+    T, d = shape
+    lddy = _rows_like(dY, dtype, shape, "dY")
+    lddh = d if dH is None else _rows_like(dH, dtype, shape, "dH")
     if out is None:
-        out = torch.empty((T, d), dtype=H.dtype, device=H.device)
-    lddx = _matrix(out, H.dtype, T, d, "out")
+        out = torch.empty(shape, dtype=dtype, device=H.device)
+    lddx = _rows_like(out, dtype, shape, "out")
     if weight is None:
         if dw is not None:
             raise ValueError("dw: there are no weights")
@@ -1102,7 +1113,7 @@ def _expert_scales(We, scale, shape, name: str):
 def moe_layer(X, ids, weights, up: PackedExperts, up_scale, down: PackedExperts, down_scale, gate: PackedExperts | None = None,
               gate_scale=None, x_scale=None, out=None, dtype=None):
     """Y [T, d] = sum_k weights[t, k] Down(silu(Gate x_t) * Up x_t) by the experts ids[t, k] (without a gate: silu(Up x_t)),
-    for a few tokens (T K at most 1024), in two launches: the answer of the same layer strung together from scaled_linear's
+    for a few tokens (T K at most 1024), in two launches (up to four for more than 8 tokens): the answer of the same layer strung together from scaled_linear's
     products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8 with ``x_scale`` (rms_norm_quantize's
     rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a slot without an expert; weights float32
     [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with float32 scales [E, outputs]. Y is in

@@ -230,7 +230,11 @@ __device__ __forceinline__ void finish_row(const LogArgs& a, int64_t t, const St
 // A workgroup to a row's part, a chunk of NV vectors a thread at a time. Each wave
 // has statistics and candidates of its own, so that no wave waits for another
 // before the end of the part. The candidates' bound is first the k-th greatest of
-// the lanes' maxima, then that of the candidates.
+// the lanes' maxima, then that of the candidates. Two to four workgroups a CU read
+// while others add: 2048 x 131072 bf16 in 111 us (4.8 TB/s), with 20 top tokens 135
+// (the candidates take 2900 of a wave's 7800 vector instructions). Tried without
+// gain: terms of one fused operation each, a bound shared by the waves, one loop for
+// all vectors' candidates (189 us). One row: 7.5 us and 4.4 for the join.
 template <typename E, int NV>
 __global__ __launch_bounds__(NT, 4) void logprob_kernel(LogArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), CH = NT * NV * EV;
@@ -404,7 +408,8 @@ struct LogBwdArgs {
   int32_t chunks;
 };
 
-// A workgroup to a chunk of a row, NV vectors a thread.
+// A workgroup to a chunk of a row, NV vectors a thread. Bound by the bytes (2048 x
+// 131072 bf16: 214-218 us, 5.0 TB/s).
 template <typename E, int NV>
 __global__ __launch_bounds__(NT) void logprob_backward_kernel(LogBwdArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), CH = NT * NV * EV;

@@ -103,6 +103,10 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 
 // P threads to a row, each with up to NV vectors of it in registers; from 128
 // threads on a row to a workgroup, which reads a longer row's other vectors again.
+// Weights stay in registers over the rows that a workgroup takes. Bound by the
+// rows' bytes (4096 x 4096 bf16 with the residual, to int8: 27.8 us, 4.2 TB/s;
+// 131072 x 128 17 us, 3.9 TB/s; 2048 x 16384 with fp32 weights 63 us, 4.2 TB/s) and,
+// for a few rows, by a launch and two reductions (one of 5120: 4.6 us).
 template <typename E, typename W, int P, int NV, bool WHOLE>
 __global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_kernel(NormArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), TB = P > 64 ? P : NT, RPB = TB / P;
@@ -278,7 +282,9 @@ constexpr int FT = 16;  // values of a row that a thread has
 // P threads to a row, FT values each; a row to a workgroup from 128 threads on. A
 // thread has the same columns in every row that its workgroup takes (a stride of
 // the grid apart), so the columns' dw stay in its registers; a workgroup's sums
-// go to a row of `part`.
+// go to a row of `part`. Bound by the rows' bytes (8192 x 4096 bf16 with dh: 51 us
+// and 4.7 for the sums of `part`, 4.8 TB/s; 1500 x 1111 fp32, rows at any address and
+// partly from the MALL, 11.5 and 5).
 template <typename E, typename W, int P, bool WHOLE>
 __global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_backward_kernel(NormBwdArgs a) {
   constexpr int EV = 16 / (int)sizeof(E), NV = FT / EV, TB = P > 64 ? P : NT, RPB = TB / P;
