@@ -203,9 +203,11 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
                             const int32_t* rows, const float* w, int32_t T, int32_t K, int32_t d, void* dO,
                             int64_t lddo, float* dw, hipStream_t stream);
 
-/* A mixture-of-experts layer for a few tokens in two launches (four for more
- * than 8 tokens whose rows are floats, three for int8 ones), with the products, the row quantization and the sums of the calls it stands for
- * (fp_scaled_linear by expert, twice, and fp_moe_combine):
+/* A mixture-of-experts layer for a few tokens in two launches (three, or four
+ * where rows are floats, with more than 8 tokens and more than two rows an expert
+ * or with more than 32 tokens), with the products, the row
+ * quantization and the sums of the calls it stands for (fp_scaled_linear by
+ * expert, twice, and fp_moe_combine):
  *   a[t, k] = silu(G x_t) * (U x_t)  (gate NULL: silu(U x_t)), fp32;
  *             silu(v) = v / (1 + exp(-v)); G, U the weights of expert ids[t, k]
  *   Y[t, :] = sum_k weights[t, k] D a[t, k], k ascending, fp32, rounded once
@@ -215,9 +217,10 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
  * token may name an expert twice. weights: device fp32 [T, K]. gate, up: DEVICE
  * arrays of E device pointers to each expert's weights [ff, d] from
  * fp_witness_pack_weights, with gate_scale[e ld_gate + j] and up_scale likewise;
- * down: of [d, ff], with down_scale. Y [T, d] (ldy) in y_dt; a token without
- * experts gets zeros. T K <= FP_MAX_FEW_SLOTS, E <= FP_MAX_EXPERTS, d and ff in
- * [1, FP_MAX_DIN]. ws: fp_moe_layer_workspace bytes, 256-byte aligned, contents
+ * down: of [d, ff], with down_scale. Y [T, d] (ldy) in y_dt, which may be X; a token
+ * without experts gets zeros. T K <= FP_MAX_FEW_SLOTS, E <= FP_MAX_EXPERTS, d and ff in
+ * [1, FP_MAX_DIN]; sizes whose weights would be 2^43 bytes or more are refused
+ * (FP_ESHAPE). ws: fp_moe_layer_workspace bytes, 256-byte aligned, contents
  * on entry do not matter. */
 int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const float* x_scale, const void* ids, int32_t id_bytes,
                  const float* weights, int32_t T, int32_t K, int32_t E, const int8_t* const* gate,

@@ -65,7 +65,8 @@ def layer(x=BF16, X=D, ldx=64, xs=None, ids=D, b=4, w=D, T=4, K=2, E=8, g=D, gs=
     (dict(xs=TWO), EARG), (dict(gs=TWO), EARG), (dict(us=TWO), EARG), (dict(ds=TWO), EARG), (dict(g=ctypes.c_void_p(260)), EARG), (dict(u=ctypes.c_void_p(260)), EARG),
     (dict(dn=ctypes.c_void_p(260)), EARG), (dict(ws=ctypes.c_void_p(128)), EARG), (dict(ws=None), EWS), (dict(n=4096), EWS),
     (dict(T=513), ESHAPE), (dict(T=1 << 30, K=1 << 30), ESHAPE), (dict(d=0), ESHAPE), (dict(ff=0), ESHAPE), (dict(d=131072, ldx=131072, ldy=131072, ldd=131072), ESHAPE),
-    (dict(ff=131072, ldu=131072, ldg=131072), ESHAPE), (dict(ldx=63), ESHAPE), (dict(ldy=63), ESHAPE), (dict(ldu=95), ESHAPE), (dict(ldg=95), ESHAPE), (dict(ldd=63), ESHAPE)])
+    (dict(ff=131072, ldu=131072, ldg=131072), ESHAPE),
+    (dict(T=1024, K=1, E=1024, d=131071, ff=131071, ldx=131071, ldy=131071, ldd=131071, ldu=131071, ldg=131071), ESHAPE), (dict(ldx=63), ESHAPE), (dict(ldy=63), ESHAPE), (dict(ldu=95), ESHAPE), (dict(ldg=95), ESHAPE), (dict(ldd=63), ESHAPE)])
 def test_moe_layer(kw, code):
     assert layer(**kw) == code
     assert b"fp_moe_layer" in fp.lib().fp_last_error()

@@ -93,7 +93,7 @@ def route(g, T, K, E, drop=0.0, wide=False):
 CASES = [(1, 1, 1, 64, 64), (1, 8, 128, 256, 128), (2, 2, 4, 1, 1), (3, 2, 5, 15, 17), (8, 2, 16, 512, 768), (5, 4, 33, 63, 31),
          (9, 1, 3, 65, 33), (16, 2, 4, 100, 257), (33, 1, 1, 128, 96), (61, 3, 20, 200, 333), (64, 16, 40, 48, 64), (64, 1, 2, 1000, 130),
          (1, 16, 600, 40, 40), (7, 3, 1024, 24, 40), (1024, 1, 12, 32, 64), (10, 100, 7, 64, 32), (4, 2, 6, 2100, 1029), (12, 5, 9, 129, 2050), (2, 1, 3, 64, 5000), (8, 8, 64, 640, 2100),
-         (20, 1, 3, 64, 5000), (40, 2, 60, 640, 1100)]
+         (20, 1, 3, 64, 5000), (40, 2, 60, 640, 1100), (32, 4, 64, 96, 160), (32, 1, 16, 200, 130), (16, 2, 16, 64, 3000)]
 
 
 @pytest.mark.parametrize("T,K,E,d,ff", CASES)
@@ -118,10 +118,16 @@ def test_same_experts(fp):
     g = torch.Generator("cuda").manual_seed(4)
     L = Layer(fp, g, 6, 96, 160, True)
     X = tokens(g, 40, 96, torch.float32)
-    ids = torch.tensor([[2, 2, 5]], dtype=torch.int32, device="cuda").repeat(40, 1)
-    w = torch.rand((40, 3), generator=g, device="cuda")
-    q, s = fp.quantize_rows(X)
-    L.check(L(fp, X, ids, w), q, s, ids, w)
+    for T in (40, 8, 3):  # with few tokens too an expert has more than eight rows
+        ids = torch.tensor([[2, 2, 5]], dtype=torch.int32, device="cuda").repeat(T, 1)
+        w = torch.rand((T, 3), generator=g, device="cuda")
+        q, s = fp.quantize_rows(X[:T])
+        L.check(L(fp, X[:T], ids, w), q, s, ids, w)
+    L = Layer(fp, g, 64, 96, 160, False)  # 32 tokens, two rows an expert on average, all of them with two experts
+    ids = torch.tensor([[7, 60, 7, 60]], device="cuda").repeat(32, 1)
+    w = torch.rand((32, 4), generator=g, device="cuda")
+    q, s = fp.quantize_rows(X[:32])
+    L.check(L(fp, X[:32], ids, w), q, s, ids, w)
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -180,6 +186,18 @@ def test_bad_rows_stay_alone(fp):
     same = [0, 2, 5, 7, 8, 9, 10, 11]
     assert torch.equal(Y[same], want[same])
     assert bool(Y[[1, 3]].isnan().all()) and bool((Y[4] == 0).all())
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_over_its_input(fp, T):
+    """Y written over X."""
+    g = torch.Generator("cuda").manual_seed(14)
+    L = Layer(fp, g, 6, 200, 90, True)
+    X = tokens(g, T, 200, torch.bfloat16)
+    ids, w = route(g, T, 2, 6)
+    want = L(fp, X, ids, w)
+    x = X.clone()
+    assert L(fp, x, ids, w, out=x) is x and torch.equal(x, want)
 
 
 def test_no_tokens(fp):

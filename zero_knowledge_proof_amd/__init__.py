@@ -811,7 +811,8 @@ def _stream_rows(X, shape, dtype, residual, residual_out):
     ldr = _rows_like(residual, dtype, shape, "residual")
     if residual_out is None:
         residual_out = torch.empty(shape, dtype=dtype, device=X.device)
-    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), _rows_like(residual_out, dtype, shape, "residual_out")
+    ldh = _rows_like(residual_out, dtype, shape, "residual_out")
+    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), ldh
 
 
 def rms_norm(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None):
@@ -1113,8 +1114,8 @@ def _expert_scales(We, scale, shape, name: str):
 def moe_layer(X, ids, weights, up: PackedExperts, up_scale, down: PackedExperts, down_scale, gate: PackedExperts | None = None,
               gate_scale=None, x_scale=None, out=None, dtype=None):
     """Y [T, d] = sum_k weights[t, k] Down(silu(Gate x_t) * Up x_t) by the experts ids[t, k] (without a gate: silu(Up x_t)),
-    for a few tokens (T K at most 1024), in two launches (up to four for more than 8 tokens): the answer of the same layer strung together from scaled_linear's
-    products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8 with ``x_scale`` (rms_norm_quantize's
+    for a few tokens (T K at most 1024), in two launches (up to four where an expert has many): the answer of the same layer
+    strung together from scaled_linear's products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8 with ``x_scale`` (rms_norm_quantize's
     rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a slot without an expert; weights float32
     [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with float32 scales [E, outputs]. Y is in
     ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: an X or weights that require one are refused

@@ -19,8 +19,8 @@
 // The second cuts its ranges inside panels: the parts of a product are added as
 // integers, in any order, and the last workgroup to arrive at 32 outputs scales
 // and adds the experts' products of every token in the order of its choices. For
-// more than FEW tokens, whose rows an expert's workgroups would each quantize
-// again, two launches between do that once.
+// more rows, which an expert's workgroups would each quantize again, two launches
+// between do that once.
 //
 // Bound by the weights' bytes where there are many (8 tokens of 2 of 16 experts, 4096
 // -> 14336 -> 4096: 206 and 112 us, 5.7 and 5.8 TB/s) and by one read after another
@@ -30,7 +30,7 @@
 // one token: a workgroup to an expert and panel with a prologue each 398 and 32; equal
 // ranges of panels 349 and 23; the outputs' panels cut 316 and 23. With eight waves a
 // workgroup the same; pairs of panels in the second launch 2 us faster for one token,
-// 15% slower for 32 tokens.
+// 13% slower for 32 tokens.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
@@ -41,7 +41,6 @@
 namespace {
 
 constexpr int SLOTS = FP_MAX_FEW_SLOTS;   // T K
-constexpr int FEW = 8;                    // tokens whose rows are quantized where they are multiplied
 constexpr int RP = 36;                    // LDS words of a row's sums
 
 // Global memory, which the compiler does not see of an address that it reads from
@@ -276,8 +275,8 @@ struct Piece {
 };
 
 // A range of units, [from, to) of a stream in which panel t has [t NU, (t + 1) NU).
-// All of a launch's units are at most FP_MAX_EXPERTS * 2^12 * 2^9 = 2^31. (Divisions
-// in 64 bits took 1 us of a workgroup's 10.)
+// All of a launch's units fit 31 bits (the host sees to it): divisions in 64 bits are
+// a good part of a small launch.
 struct Range {
   uint32_t from, to;
 };
@@ -626,17 +625,22 @@ Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
   s.part = take(N * d * 4);
   s.A = take(N * chunked(ff) * 4);
   s.xs_out = take(N * ((d + 31) / 32) * 4);
-  if (T <= FEW) {
-    s.top = take(N * ((ff + 127) / 128 * 4) * 4);
-  } else {
-    s.xs = take(T * 4);
-    s.xq = take(T * chunked(d));
-    s.as = take(N * 4);
-    s.aq = take(N * chunked(ff));
-  }
+  s.top = take(N * ((ff + 127) / 128 * 4) * 4);
+  s.xs = take(T * 4);
+  s.xq = take(T * chunked(d));
+  s.as = take(N * 4);
+  s.aq = take(N * chunked(ff));
   s.bytes = at;
   return s;
 }
+
+// Rows quantized where they are multiplied, eight of an expert at a time (more read
+// the weights again): no expert has more than eight of 8 tokens, each with its own
+// experts, and few experts do of 32 with two rows an expert on average (16 tokens, 4
+// of 64, 1024 -> 512 -> 1024: 30 us, quantized between 35; 32 tokens of 4 of 64, 2048
+// -> 1024 -> 2048: 95, so 111; with more rows, 61 tokens, 3 of 20: 90, so 51;
+// skewed, 32 tokens of 1 of 16, 4096 -> 4096 -> 4096: 145, so 126).
+bool few_rows(int32_t T, int32_t K, int32_t E) { return T <= 8 || (T <= 32 && T * K <= 2 * E); }
 
 int check_sizes(const char* fn, int32_t T, int32_t K, int32_t d, int32_t ff) {
   if (T < 0 || K < 1 || d < 0 || ff < 0) return fpi::fail(FP_EARG, "%s: T=%d K=%d d=%d ff=%d", fn, T, K, d, ff);
@@ -692,6 +696,10 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   if (ldx < d || ldy < d) return fpi::fail(FP_ESHAPE, "%s: leading dimension too small", fn);
   if (ld_up < ff || ld_down < d || (gate && ld_gate < ff)) return fpi::fail(FP_ESHAPE, "%s: leading dimension of the scales too small", fn);
   if (!gate != !gate_scale) return fpi::fail(FP_EARG, "%s: gate and its scales come together", fn);
+  // units of the launches (of at least 4 KiB of weights) are counted in 31 bits
+  const int64_t met = (int64_t)T * K < E ? (int64_t)T * K : E;
+  if (met * ((ff + 31) / 32) * ((d + 127) / 128) > 0x7FFFFFFF || met * ((d + 31) / 32) * ((ff + 127) / 128) > 0x7FFFFFFF)
+    return fpi::fail(FP_ESHAPE, "%s: %lld experts of d=%d ff=%d", fn, (long long)met, d, ff);
   if (T == 0) return fpi::ok();
   if (!X || !ids || !weights || !up || !up_scale || !down || !down_scale || !Y || (x_dt == FP_I8 && !x_scale))
     return fpi::fail(FP_EARG, "%s: null pointer", fn);
@@ -703,7 +711,7 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   if (!ws || ws_bytes < s.bytes) return fpi::fail(FP_EWORKSPACE, "%s: workspace %zu < %zu", fn, ws ? ws_bytes : 0, s.bytes);
   if ((uintptr_t)ws % 256) return fpi::fail(FP_EARG, "%s: workspace not 256-byte aligned", fn);
   char* const w = (char*)ws;
-  const bool few = T <= FEW;
+  const bool few = few_rows(T, K, E);
   bool whole = d % 16 == 0;
   if (!few && x_dt != FP_I8) {
     const int r = fp_quantize_rows(x_dt, X, ldx, T, d, (int8_t*)(w + s.xq), chunked(d), (float*)(w + s.xs), stream);
