@@ -83,12 +83,17 @@ struct FewArgs {
 };
 
 template <typename XT>
-constexpr int rows_of() { return sizeof(XT) == 1 ? 32 : 8; }  // of an expert at a time: 8 where they are quantized here
+constexpr int rows_of() { return sizeof(XT) == 1 ? 16 : 8; }  // of an expert at a time: 8 where they are quantized here
+// Workgroups that a CU holds (16 rows and four workgroups, 64 tokens of 8 of 128, 2048
+// -> 768 -> 2048: 194 us, with three 218, with 32 rows and three 239; 61 tokens of 3 of
+// 20, with up to 40 rows an expert: 54, 53 and 51; floats need more registers than
+// four leave them).
+template <typename XT>
+constexpr int wgs_of() { return sizeof(XT) == 1 ? 4 : 3; }
 constexpr int NW = 4, NT = NW * 64;  // waves, each with units of K in turn
-constexpr int WGS = 3;               // workgroups that a CU holds
 constexpr int CUS = 256;
 
-// A unit of K: the blocks of it that a wave takes together (two for 32 rows, for the
+// A unit of K: the blocks of it that a wave takes together (two for 16 rows, for the
 // sake of LDS).
 template <int MAPS, int ROWS>
 struct Unit {
@@ -414,14 +419,14 @@ __device__ __forceinline__ void experts_of(const FewArgs& a, uint32_t first, uin
 // whole ones would leave many workgroups idle and the parts are worth their
 // additions: with fewer panels than CUs, or with a last round that few workgroups
 // have (8 tokens of 2 of 16 experts, 14336 -> 4096: 110 us, uncut 140; 61 tokens of 3
-// of 20, 2003 -> 1000, cut 38 us, uncut 24).
+// of 20, 2003 -> 1000, cut 43 us, uncut 25).
 __device__ __forceinline__ bool cut_panels(const FewArgs& a, int present) {
   const uint32_t panels = (uint32_t)present * a.out_panels, rounds = (panels + a.out_grid - 1) / a.out_grid;
   return a.out_units >= 2 * NW && (panels < CUS || (rounds > 1 && (uint64_t)panels * 10 < (uint64_t)rounds * a.out_grid * 9));
 }
 
 template <int MAPS, typename XT, bool WHOLE>
-__global__ __launch_bounds__(NT, WGS) void moe_hidden_kernel(FewArgs a) {
+__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_hidden_kernel(FewArgs a) {
   using L = Lds<MAPS, XT>;
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
@@ -498,7 +503,7 @@ __device__ __forceinline__ void store_out(const FewArgs& a, int t, int o, float 
 // with a.xs. Uncut products go to `part` scaled, cut ones as integers, with the
 // rows' scales.
 template <typename XT>
-__global__ __launch_bounds__(NT, WGS) void moe_output_kernel(FewArgs a) {
+__global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a) {
   using L = Lds<1, XT>;
   constexpr int ROWS = L::ROWS;
   __shared__ L lds;
@@ -638,8 +643,8 @@ Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
 // the weights again): no expert has more than eight of 8 tokens, each with its own
 // experts, and few experts do of 32 with two rows an expert on average (16 tokens, 4
 // of 64, 1024 -> 512 -> 1024: 30 us, quantized between 35; 32 tokens of 4 of 64, 2048
-// -> 1024 -> 2048: 95, so 111; with more rows, 61 tokens, 3 of 20: 90, so 51;
-// skewed, 32 tokens of 1 of 16, 4096 -> 4096 -> 4096: 145, so 126).
+// -> 1024 -> 2048: 96, so 102; with more rows, 61 tokens, 3 of 20: 90, so 54;
+// skewed, 32 tokens of 1 of 16, 4096 -> 4096 -> 4096: 156, so 148).
 bool few_rows(int32_t T, int32_t K, int32_t E) { return T <= 8 || (T <= 32 && T * K <= 2 * E); }
 
 int check_sizes(const char* fn, int32_t T, int32_t K, int32_t d, int32_t ff) {
@@ -652,13 +657,14 @@ int check_sizes(const char* fn, int32_t T, int32_t K, int32_t d, int32_t ff) {
 
 // As many workgroups as the GPU holds at once, if the experts that the tokens can
 // meet have `parts` for them.
+template <typename XT>
 dim3 few_grid(int64_t parts) {
-  const int64_t held = CUS * WGS;
+  const int64_t held = CUS * wgs_of<XT>();
   return dim3((unsigned)(parts < held ? parts : held));
 }
 template <int MAPS, typename XT>
 void launch_hidden_rows(const FewArgs& a, int64_t most, bool whole, hipStream_t st) {
-  const dim3 grid = few_grid(most * a.panels), block(NT);
+  const dim3 grid = few_grid<XT>(most * a.panels), block(NT);
   if (whole) moe_hidden_kernel<MAPS, XT, true><<<grid, block, 0, st>>>(a);
   else moe_hidden_kernel<MAPS, XT, false><<<grid, block, 0, st>>>(a);
 }
@@ -731,7 +737,8 @@ extern "C" int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const flo
   const int blocks = few ? Unit<1, rows_of<float>()>::BLOCKS : Unit<1, rows_of<int8_t>()>::BLOCKS;
   h.out_panels = (d + 31) / 32;
   h.out_units = ((ff + WP_BK - 1) / WP_BK + blocks - 1) / blocks;
-  h.out_grid = (int32_t)few_grid(most * h.out_panels * h.out_units).x;
+  const int64_t parts = most * h.out_panels * h.out_units;
+  h.out_grid = (int32_t)(few ? few_grid<float>(parts) : few_grid<int8_t>(parts)).x;
   h.A = (float*)(w + s.A);
   h.lda = chunked(ff);
   h.top = few ? (float*)(w + s.top) : nullptr;
