@@ -205,9 +205,9 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
 
 /* A mixture-of-experts layer for a few tokens in two launches (three, or four
  * where rows are floats, with more than 8 tokens and more than two rows an expert
- * or with more than 32 tokens), with the products, the row
- * quantization and the sums of the calls it stands for (fp_scaled_linear by
- * expert, twice, and fp_moe_combine):
+ * or with more than 32 tokens), with the products, the row quantization and the
+ * sums of the calls it stands for (fp_scaled_linear by expert, twice, and
+ * fp_moe_combine):
  *   a[t, k] = silu(G x_t) * (U x_t)  (gate NULL: silu(U x_t)), fp32;
  *             silu(v) = v / (1 + exp(-v)); G, U the weights of expert ids[t, k]
  *   Y[t, :] = sum_k weights[t, k] D a[t, k], k ascending, fp32, rounded once

@@ -153,7 +153,8 @@ def test_binding_moe_layer():
                dict(gate=pack(4, 41, 64), gate_scale=us), dict(gate=up, gate_scale=us[:, 1:]), dict(out=torch.zeros(3, 63)), dict(out=torch.zeros(3, 64, dtype=torch.int8)),
                dict(dtype=torch.int8)):
         refused(fp.moe_layer, **dict(ok, **kw))
-    for kw in (dict(X=X.clone().requires_grad_()), dict(weights=w.clone().requires_grad_())):
+    for kw in (dict(X=X.clone().requires_grad_()), dict(weights=w.clone().requires_grad_()), dict(up_scale=us.clone().requires_grad_()),
+               dict(down_scale=ds.clone().requires_grad_()), dict(gate=up, gate_scale=us.clone().requires_grad_())):
         refused(fp.moe_layer, match="gradient", **dict(ok, **kw))
     if not torch.cuda.is_available():
         with pytest.raises(Exception):  # tensors that are on no device

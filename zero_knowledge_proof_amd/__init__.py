@@ -1115,14 +1115,15 @@ def moe_layer(X, ids, weights, up: PackedExperts, up_scale, down: PackedExperts,
               gate_scale=None, x_scale=None, out=None, dtype=None):
     """Y [T, d] = sum_k weights[t, k] Down(silu(Gate x_t) * Up x_t) by the experts ids[t, k] (without a gate: silu(Up x_t)),
     for a few tokens (T K at most 1024), in two launches (up to four where an expert has many): the answer of the same layer
-    strung together from scaled_linear's products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8 with ``x_scale`` (rms_norm_quantize's
-    rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a slot without an expert; weights float32
-    [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with float32 scales [E, outputs]. Y is in
-    ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: an X or weights that require one are refused
-    unless under torch.no_grad."""
-    if (X.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
-        raise ValueError("X or weights require a gradient, which this layer does not have: train through moe_dispatch and "
-                         "moe_combine, or detach them")
+    strung together from scaled_linear's products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8
+    with ``x_scale`` (rms_norm_quantize's rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a
+    slot without an expert; weights float32 [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with
+    float32 scales [E, outputs]. Y is in ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: tensors
+    that require one are refused unless under torch.no_grad."""
+    for t in (X, weights, x_scale, up_scale, down_scale, gate_scale):
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a tensor requires a gradient, which this layer does not have: train through moe_dispatch and "
+                             "moe_combine, or detach the tensor")
     if X.dim() != 2:
         raise ValueError("X: shape %s, expected two dimensions" % (tuple(X.shape),))
     T, d = X.shape
