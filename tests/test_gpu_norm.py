@@ -302,3 +302,22 @@ def test_streams_and_graphs(fp):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
         assert all(torch.equal(a, b) for a, b in zip(other, want[(i + 1) % 4]))
+
+
+@pytest.mark.parametrize("size_h,size_g,eps", [(1e15, 1e25, 1e-5), (1.0, 1e37, 1e-5), (2.0 ** 90, 1e25, 1e-5), (2.0 ** 66, 1e-15, 1e-5), (1e15, 0.0, 1e-5), (1e30, 0.0, 1e-5),
+                                               (1e-15, 1e-28, 1e-30)])
+@pytest.mark.parametrize("d", [1, 40, 300, 1200, 4096, 16384])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_far_from_one(fp, size_h, size_g, eps, d, dtype):
+    """A row whose products with its gradient leave fp32's range, or fall below it, where the row's own gradient does not;
+    the ordinary rows beside it keep theirs."""
+    g = torch.Generator("cuda").manual_seed(d)
+    H, dY = torch.randn((3, d), generator=g, device="cuda"), torch.randn((3, d), generator=g, device="cuda").clamp(-3, 3)
+    w = 1 + 0.3 * torch.rand(d, generator=g, device="cuda")
+    plain = fp.rms_norm_backward(dY.to(dtype), H.to(dtype), w, eps=eps)[0]
+    H[1] *= size_h
+    dY[1] *= size_g
+    H, dY = H.to(dtype), dY.to(dtype)
+    dx, dw = fp.rms_norm_backward(dY, H, w, eps=eps)
+    assert torch.equal(dx[[0, 2]], plain[[0, 2]])
+    check_gradients(dx, dw, dY, H, w, eps, None)

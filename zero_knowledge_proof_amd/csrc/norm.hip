@@ -10,7 +10,8 @@
 //   dx = s (g - n mean_j(g_j n_j)) + dh,   dw_j = sum_t dy_tj n_tj.
 // Sums are fp32. Where a row's sum of squares leaves fp32 though its values are
 // finite, the row is first multiplied by 2^-80 (exact but for values that vanish
-// beside the others), eps being nothing beside such a mean.
+// beside the others), eps being nothing beside such a mean. The gradient's sum of
+// g h is kept in range likewise.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
@@ -278,6 +279,7 @@ struct NormBwdArgs {
 };
 
 constexpr int FT = 16;  // values of a row that a thread has
+constexpr float LIFT = 0x1p60f;
 
 // P threads to a row, FT values each; a row to a workgroup from 128 threads on. A
 // thread has the same columns in every row that its workgroup takes (a stride of
@@ -316,6 +318,7 @@ __global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_backward_kernel(Norm
       const float y = load_elem<E>(ry[v], e);
       return a.w ? y * w[v].at(e) : y;
     };
+    // sd is sum_j g_j h_j 2^60: no product falls below fp32's range where n does not
     float ss = 0.f, sd = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -323,30 +326,37 @@ __global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_backward_kernel(Norm
       for (int e = 0; e < EV; ++e) {
         const float h = load_elem<E>(rh[v], e);
         ss = __builtin_fmaf(h, h, ss);
-        sd = __builtin_fmaf(g(v, e), h, sd);
+        sd = __builtin_fmaf(g(v, e), h * LIFT, sd);
       }
     ss = row_reduce<P, false>(ss, red[0][turn]);
     sd = row_reduce<P, false>(sd, red[1][turn]);
-    float pre = 1.f, s;
-    if (ss < __builtin_inff()) {
+    float pre = 1.f, s, m;
+    if (ss < __builtin_inff() && fabsf(sd) < __builtin_inff()) {
       s = 1.0f / sqrtf(ss * a.inv_d + a.eps);
-    } else {  // uniform over the row's threads
-      pre = SHRINK;
+      m = (sd * (s / LIFT)) * a.inv_d;
+    } else {  // a sum above the range: again of smaller factors (uniform over the row's threads)
+      const float less = fabsf(sd) < __builtin_inff() ? 1.f : 0x1p-72f;
+      pre = ss < __builtin_inff() ? 1.f : SHRINK;
       ss = sd = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        // 1024 threads lack the registers to keep the floats for these sums: they convert anew
+        // (where there are registers it only costs: 65536 x 256 bf16 27 us, so 25)
+        if constexpr (P == 1024) asm volatile("" : "+v"(rh[v]), "+v"(ry[v]));
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
           const float h = load_elem<E>(rh[v], e) * pre;
           ss = __builtin_fmaf(h, h, ss);
-          sd = __builtin_fmaf(g(v, e), h, sd);
+          sd = __builtin_fmaf(g(v, e) * less, h, sd);
         }
+      }
       if constexpr (P > 64) __syncthreads();  // an earlier row's sums in redo are read
       ss = row_reduce<P, false>(ss, redo[0]);
       sd = row_reduce<P, false>(sd, redo[1]);
-      s = 1.0f / sqrtf(ss * a.inv_d);
+      s = 1.0f / sqrtf(ss * a.inv_d + a.eps * pre * pre);
+      m = (sd * s) * a.inv_d / less;
     }
-    const float m = (sd * s) * a.inv_d, sp = s * pre;
+    const float sp = s * pre;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float dx[EV];
