@@ -379,3 +379,54 @@ def test_decoding_step(fp):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager[i]))
+
+
+def test_packing_does_not_wait(fp):
+    """Packing the experts leaves the host free: neither the weights nor the addresses wait for the device."""
+    W = torch.randint(-8, 8, (5, 40, 70), device="cuda", dtype=torch.int8)
+    torch.cuda.synchronize()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        P = fp.pack_experts(W)
+        Q = fp.PackedExperts(P.weights)
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    for experts in (P, Q):
+        assert experts.table.tolist() == [w.data.data_ptr() for w in P.weights]
+
+
+def test_packed_on_another_stream(fp):
+    """Experts put together behind other work on one stream and used at once on another: the layer waits for their addresses."""
+    g = torch.Generator("cuda").manual_seed(21)
+    L = Layer(fp, g, 6, 96, 160, True)
+    X = tokens(g, 5, 96, torch.bfloat16)
+    ids, w = route(g, 5, 2, 6)
+    want = L(fp, X, ids, w)
+    A = torch.randn((4096, 4096), generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            A = A @ A / 64
+        again = {k: fp.PackedExperts(p.weights) for k, p in L.P.items()}
+    Y = fp.moe_layer(X, ids, w, again["up"], L.s["up"], again["down"], L.s["down"], gate=again["gate"], gate_scale=L.s["gate"])
+    assert torch.equal(Y, want)
+    torch.cuda.synchronize()
+
+
+def test_packed_and_captured_at_once(fp):
+    """The first call with newly packed experts is inside a capture."""
+    g = torch.Generator("cuda").manual_seed(22)
+    L, M = (Layer(fp, g, 6, 96, 160, True) for _ in range(2))
+    X = tokens(g, 5, 96, torch.bfloat16)
+    ids, w = route(g, 5, 2, 6)
+    M(fp, X, ids, w)  # (libraries are loaded outside of captures)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = L(fp, X, ids, w)
+    want = L(fp, X, ids, w)
+    for _ in range(3):
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)

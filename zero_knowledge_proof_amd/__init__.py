@@ -901,9 +901,9 @@ class PackedExperts:
         # (first expert, how many, their addresses in ptrs): a launch takes MAX_GROUPS
         counts = [(g, min(MAX_GROUPS, len(weights) - g)) for g in range(0, len(weights), MAX_GROUPS)]
         self.parts = [(g, n, (ctypes.c_void_p * n).from_buffer(self.ptrs, g * ctypes.sizeof(ctypes.c_void_p))) for g, n in counts]
-        self._table = None
+        self._table = self._sent = None
         if not self._capturing():
-            self.table  # now, so that a call may be captured
+            self._send()  # now, so that a call may be captured
 
     def __len__(self):
         return len(self.weights)
@@ -911,13 +911,29 @@ class PackedExperts:
     def _capturing(self) -> bool:
         return self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
 
+    def _send(self):
+        """The addresses on their way to the device, behind what the current stream has; the host does not wait."""
+        on_gpu = self.device.type == "cuda"
+        host = torch.empty(len(self.weights), dtype=torch.int64, pin_memory=on_gpu)
+        ctypes.memmove(host.data_ptr(), self.ptrs, ctypes.sizeof(self.ptrs))
+        self._table = host.to(self.device, non_blocking=True)
+        if on_gpu:
+            self._sent = torch.cuda.Event()
+            self._sent.record(torch.cuda.current_stream(self.device))
+
     @property
     def table(self):
-        """The weights' addresses on the device (int64 [G]), for calls whose experts only the device knows."""
+        """The weights' addresses on the device (int64 [G]), for calls whose experts only the device knows. The current
+        stream waits for them where they are still on their way."""
         if self._table is None:
             if self._capturing():
                 raise ValueError("experts packed inside a capture: their addresses reach the device only outside of one")
-            self._table = torch.tensor([w.data.data_ptr() for w in self.weights], dtype=torch.int64).to(self.device)
+            self._send()
+        if self._sent is not None and not self._capturing():  # (torch.cuda.graph has waited for the device)
+            if self._sent.query():
+                self._sent = None
+            else:
+                self._sent.wait(torch.cuda.current_stream(self.device))
         return self._table
 
 
