@@ -343,8 +343,8 @@ int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* R, int64_t 
  *   dX = (dY w - n mean(dY w n)) / sqrt(mean(h^2) + eps) + dH  (dH NULL: 0)
  *   dw[j] = sum_t dY[t, j] n[t, j]   (device fp32 [d], or NULL)
  * in fp32, summed in an order fixed by T, d and the type. dX is also the gradient
- * of X and R, dH that of the stream's later use; dX may be dY, H or dH. d <=
- * FP_MAX_NORM. ws: fp_rms_norm_backward_workspace bytes if dw is given (else
+ * of X and R, dH that of the stream's later use; dX may be dY, H or dH, with the
+ * same leading dimension. d <= FP_MAX_NORM. ws: fp_rms_norm_backward_workspace bytes if dw is given (else
  * NULL), contents on entry do not matter. */
 int fp_rms_norm_backward(fp_dtype dt, const void* dY, int64_t lddy, const void* H, int64_t ldh, fp_dtype w_dt,
                          const void* w, float eps, const void* dH, int64_t lddh, int32_t T, int32_t d, void* dX,
@@ -396,7 +396,8 @@ size_t fp_token_logprobs_workspace(fp_dtype dt, int32_t T, int32_t V, int32_t to
  *   dX[t, v] = (dlogprob (1[v = token] - p_v) - dentropy p_v (log p_v + entropy))
  *              / temperature
  * in fp32, rounded once. A token outside [0, V) has no log probability and passes
- * no gradient of it; a row without any token gets zeros. dX [T, V] (lddx) may be X. */
+ * no gradient of it; a row without any token gets zeros. dX [T, V] (lddx) may be X, with
+ * the same leading dimension. */
 int fp_token_logprobs_backward(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
                                int32_t id_bytes, float temperature, const float* dlogprob, const float* dentropy,
                                const float* max, const float* logsum, const float* entropy, void* dX, int64_t lddx,

@@ -188,3 +188,21 @@ def test_gradients_are_not_lost_silently():
         with torch.no_grad(), pytest.raises(Exception) as e:  # on to the next check: these are no device tensors
             f()
         assert "backward" not in str(e.value)
+
+
+A, B = (ctypes.c_void_p(256 * i) for i in (2, 3))  # other addresses that are never dereferenced
+
+
+@pytest.mark.parametrize("call,kw", [
+    (norm, dict(Y=A, H=B, X=B, ldh=65)), (norm, dict(Y=A, H=B, R=B, ldh=65)), (norm, dict(Y=A, H=B, X=A, ldy=72)), (norm, dict(Y=A, H=None, R=A, ldr=72)),
+    (norm_bwd, dict(dX=A, dY=A, lddx=65)), (norm_bwd, dict(dX=A, H=A, lddx=65)), (norm_bwd, dict(dX=A, dH=A, lddh=65)),
+    (norm_bwd, dict(dX=A, dY=A, H=B, dH=None, lddy=72))])
+def test_in_place_needs_the_same_rows(call, kw):
+    """An output at an input's address has its rows where the input has its own: else a row is overwritten before it is read."""
+    assert call(**kw) == EARG
+    assert b"leading dimension" in fp.lib().fp_last_error()
+
+
+def test_logits_in_place_need_the_same_rows():
+    assert fp.lib().fp_token_logprobs_backward(BF16, A, 500, 4, 500, D, 4, 1.0, D, D, D, D, D, A, 512, None) == EARG
+    assert b"leading dimension" in fp.lib().fp_last_error()

@@ -16,6 +16,12 @@ int ok();
 // Checks hipGetLastError() after a launch.
 int check_launch(const char* what);
 
+// Whether an output of rows in an input's place has them where the input has its
+// own (a workgroup would write over rows that another has yet to read).
+inline bool same_rows(const void* out, int64_t ldo, const void* in, int64_t ldi, int32_t rows) {
+  return !out || out != in || ldo == ldi || rows < 2;
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Limb folds on the matrix cores. With digit rows D [N, K] (N = 8 R: row

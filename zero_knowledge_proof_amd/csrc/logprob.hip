@@ -565,6 +565,7 @@ extern "C" int fp_token_logprobs_backward(fp_dtype dt, const void* X, int64_t ld
   if (((uintptr_t)dlogprob | (uintptr_t)dentropy | (uintptr_t)max | (uintptr_t)logsum | (uintptr_t)entropy) % 4 ||
       (uintptr_t)dX % elem_bytes(dt))
     return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  if (!fpi::same_rows(dX, lddx, X, ldx, T)) return fpi::fail(FP_EARG, "%s: an output in an input's place with another leading dimension", fn);
   const LogBwdArgs a{X, ldx, T, V, tokens, id_bytes == 8, 1.0f / temperature, dlogprob, dentropy, max, logsum, entropy, dX, lddx, 0};
   if (dt == FP_F32) launch_backward<float>(a, stream);
   else if (dt == FP_F16) launch_backward<__half>(a, stream);

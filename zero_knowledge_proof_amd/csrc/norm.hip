@@ -521,6 +521,9 @@ extern "C" int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* 
   if (d > 0 && !Y && !Xq) return fpi::fail(FP_EARG, "%s: no output", fn);
   if (d > 0 && !Xq != !scale) return fpi::fail(FP_EARG, "%s: int8 rows and their scales come together", fn);
   if ((uintptr_t)scale % 4) return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  if (d > 0 && !(fpi::same_rows(H, ldh, X, ldx, T) && fpi::same_rows(H, ldh, R, ldr, T) && fpi::same_rows(Y, ldy, X, ldx, T) &&
+                 fpi::same_rows(Y, ldy, R, ldr, T)))
+    return fpi::fail(FP_EARG, "%s: an output in an input's place with another leading dimension", fn);
   NormArgs a{X, ldx, R, ldr, w, eps, d ? 1.0f / (float)d : 0.f, T, d, H, ldh, Y, ldy, Xq, ldq, scale};
   if (d == 0) a.Q = (int8_t*)scale;  // no element is written: the scales of empty rows, 0
   return launch_norm_types(dt, w_dt, a, stream);
@@ -545,6 +548,8 @@ extern "C" int fp_rms_norm_backward(fp_dtype dt, const void* dY, int64_t lddy, c
   if (dw && need && (!ws || ws_bytes < need)) return fpi::fail(FP_EWORKSPACE, "%s: workspace %zu < %zu", fn, ws ? ws_bytes : 0, need);
   if ((uintptr_t)ws % 4 || (uintptr_t)dw % 4) return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
   if (d == 0) return fpi::ok();
+  if (!(fpi::same_rows(dX, lddx, dY, lddy, T) && fpi::same_rows(dX, lddx, H, ldh, T) && fpi::same_rows(dX, lddx, dH, lddh, T)))
+    return fpi::fail(FP_EARG, "%s: an output in an input's place with another leading dimension", fn);
   const NormBwdArgs a{dY, lddy, H, ldh, w, dH, lddh, eps, 1.0f / (float)d, T, d, dX, lddx, dw ? (float*)ws : nullptr};
   if (T > 0) {
     if (dt == FP_F32) launch_bwd<float, float>(a, stream);
