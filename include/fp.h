@@ -332,8 +332,9 @@ size_t fp_scaled_linear_workspace(int32_t T, int32_t d_in);
  * X, R, H, Y [T, d] in dt (FP_F32, FP_F16 or FP_BF16), each with a leading
  * dimension; w [d] in dt or FP_F32 (w_dt); Xq int8, scale fp32 [T]. Y or Xq must
  * be given. eps in [1e-30, 1], d <= FP_MAX_DIN. H may be R or X, and Y may be X
- * or R, with the same leading dimension. A row with a NaN or an infinity gives
- * NaN where it stands (zeros beside an infinity, NaN beside a NaN) and scale NaN. */
+ * or R, with the same leading dimension, and not both the same one. A row with a
+ * NaN or an infinity gives NaN where it stands (zeros beside an infinity, NaN
+ * beside a NaN) and scale NaN. */
 int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* R, int64_t ldr, fp_dtype w_dt, const void* w,
                 float eps, int32_t T, int32_t d, void* H, int64_t ldh, void* Y, int64_t ldy, int8_t* Xq, int64_t ldq,
                 float* scale, hipStream_t stream);

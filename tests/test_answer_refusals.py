@@ -206,3 +206,9 @@ def test_in_place_needs_the_same_rows(call, kw):
 def test_logits_in_place_need_the_same_rows():
     assert fp.lib().fp_token_logprobs_backward(BF16, A, 500, 4, 500, D, 4, 1.0, D, D, D, D, D, A, 512, None) == EARG
     assert b"leading dimension" in fp.lib().fp_last_error()
+
+
+def test_stream_and_norm_need_places_of_their_own():
+    """H may be X and Y may be X, but not both: one of them would be lost."""
+    assert norm(X=A, H=A, Y=A) == EARG and norm(R=A, H=A, Y=A) == EARG and norm(H=A, Y=A) == EARG
+    assert b"same place" in fp.lib().fp_last_error()

@@ -818,8 +818,8 @@ def _stream_rows(X, shape, dtype, residual, residual_out):
 def rms_norm(X, weight, eps: float = 1e-5, residual=None, residual_out=None, out=None):
     """Y = h / sqrt(mean(h^2) + eps) * weight for the rows h of X [T, d] (float32, float16 or bfloat16), in X's type; weight
     [d] in X's type or float32 (None: ones). With a ``residual`` h = X + residual, and (Y, H) is returned, H being the sum
-    in X's type (``residual_out``, which may be the residual itself or X); the norm is of the sum before that rounding.
-    Sums in fp32. The gradient is rms_norm_backward; no graph is recorded, and tensors that require a gradient are refused
+    in X's type (``residual_out``, which may be the residual itself or X, but not ``out``); the norm is of the sum before
+    that rounding. Sums in fp32. The gradient is rms_norm_backward; no graph is recorded, and tensors that require a gradient are refused
     unless under torch.no_grad."""
     _no_graph("rms_norm_backward", X, weight, residual)
     shape, dtype, dt, ldx, w_dt, w = _norm_args(X, weight, "X")

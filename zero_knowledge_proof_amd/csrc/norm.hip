@@ -521,6 +521,7 @@ extern "C" int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* 
   if (d > 0 && !Y && !Xq) return fpi::fail(FP_EARG, "%s: no output", fn);
   if (d > 0 && !Xq != !scale) return fpi::fail(FP_EARG, "%s: int8 rows and their scales come together", fn);
   if ((uintptr_t)scale % 4) return fpi::fail(FP_EARG, "%s: misaligned pointer", fn);
+  if (d > 0 && H && H == Y) return fpi::fail(FP_EARG, "%s: the sum and its norm in the same place", fn);
   if (d > 0 && !(fpi::same_rows(H, ldh, X, ldx, T) && fpi::same_rows(H, ldh, R, ldr, T) && fpi::same_rows(Y, ldy, X, ldx, T) &&
                  fpi::same_rows(Y, ldy, R, ldr, T)))
     return fpi::fail(FP_EARG, "%s: an output in an input's place with another leading dimension", fn);
