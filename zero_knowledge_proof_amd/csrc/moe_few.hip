@@ -358,6 +358,7 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
         if (c == 0 || 8 * c < nr)
 #pragma unroll
           for (int g = 0; g < U::PIECES; ++g) *(v4i*)(xs + 8 * c * U::XP + 128 * g) = x[c][g].bytes(rs);
+      sdev::wave_sync();  // (other lanes read them)
 #pragma unroll
       for (int b = 0; b < U::BLOCKS; ++b) {
         if (b > 0 && U::BLOCKS * u + b >= NB) break;  // uniform
@@ -368,6 +369,7 @@ __device__ __forceinline__ void products(const FewArgs& a, const Weights (&W)[MA
           for (int i = 0; i < MAPS; ++i) acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i][b][q], f, acc[i], 0, 0, 0);
         }
       }
+      sdev::wave_sync();  // (the next unit's take their place)
       if (u + NW < end) load(t, u + NW);
       else load_from(t + 1);
     }

@@ -13,6 +13,15 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// Between a wave's lanes: what they wrote to LDS before it the others read after
+// it, and the other way round. No instruction (a wave's LDS accesses keep their
+// order), but the compiler keeps them in theirs.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // bf16 bits of a float, rounded to nearest even (NaN stays a quiet NaN).
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
   const uint32_t u = __float_as_uint(f);
