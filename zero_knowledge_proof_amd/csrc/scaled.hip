@@ -519,6 +519,7 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
         if (u <= last) {  // uniform
 #pragma unroll
           for (int c = 0; c < XR; ++c) *(v4i*)(xs + 8 * c * XP) = xr[p % PX][c];
+          sdev::wave_sync();  // (other lanes read them)
         }
         xload(p % PX, min(u + PX * NW, last));
         if (u <= last) {
@@ -534,6 +535,7 @@ __global__ __launch_bounds__(NW * 64) void scaled_rows_kernel(ScaledArgs a, Grou
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[p][i][q], x, acc[i][j], 0, 0, 0);
             }
           }
+          sdev::wave_sync();  // (the next unit's take their place)
         }
         wload(p, min(u + PF * NW, last));
       }
