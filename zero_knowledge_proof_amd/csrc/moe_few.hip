@@ -568,7 +568,14 @@ __global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a)
   });
 #pragma unroll
   for (int i = 0; i < 3; ++i) kept(soon[i]);
-  // each thread's additions are at the agent's level before its workgroup's arrivals count
+  // The products that another workgroup adds up (part, xs_out) are stored, added and
+  // read as agent-scope atomics only, which gfx950 carries out behind the XCDs' L2,
+  // where all of them see the same: it is enough that each thread's are done
+  // (s_waitcnt) before its workgroup's arrivals count, and that the reads come behind
+  // the last arrival and a barrier. The language has no word for this order less than
+  // release and acquire of the agent, which write back and drop the L2 with the
+  // weights in it (8 tokens of 2 of 16 experts 323 us, with them at the arrivals 353,
+  // as fences of every wave 448; one token of 8 of 128 24.5, 29 and 38).
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
   __builtin_amdgcn_s_waitcnt(0);
   const uint32_t units = (uint32_t)present * NU;  // of 32 outputs, in all experts
