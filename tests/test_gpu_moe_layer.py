@@ -430,3 +430,82 @@ def test_packed_and_captured_at_once(fp):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, want)
+
+
+def panels_of(ids, d):
+    """How many 32-output panels the second launch has: all of those of every expert that a token meets."""
+    return ids[ids >= 0].unique().numel() * ((d + 31) // 32)
+
+
+# ff short of eight units of K, so that no panel is cut, and more panels than the 768 (float rows) or 1024 (int8 rows) workgroups
+@pytest.mark.parametrize("T,K,E,d,ff,held", [(16, 4, 64, 1024, 512, 768), (32, 4, 64, 2048, 1024, 768), (5, 8, 40, 1100, 270, 768), (40, 4, 64, 1024, 512, 1024),
+                                             (64, 8, 48, 1000, 333, 1024)])
+@pytest.mark.parametrize("gate", [True, False])
+def test_whole_panels_several_to_a_workgroup(fp, T, K, E, d, ff, held, gate):
+    g = torch.Generator("cuda").manual_seed(T + d + ff)
+    L = Layer(fp, g, E, d, ff, gate, pad=5)
+    for dtype, drop in ((torch.bfloat16, 0.0), (torch.float32, 0.1)):
+        X = tokens(g, T, d, dtype)
+        ids, w = route(g, T, K, E, drop=drop)
+        assert panels_of(ids, d) > held
+        q, s = fp.quantize_rows(X)
+        Y = L(fp, X, ids, w, dtype=torch.float32)
+        L.check(Y, q, s, ids, w)
+        assert torch.equal(L(fp, q, ids, w, x_scale=s, dtype=torch.float32), Y)
+
+
+@pytest.mark.parametrize("T,K,E,d,ff", [(8, 2, 16, 512, 2048), (16, 4, 64, 1024, 512), (40, 2, 16, 512, 320), (40, 2, 16, 256, 1100)])
+def test_streams_and_graphs_of_every_way(fp, T, K, E, d, ff):
+    """Cut sums, several whole panels to a workgroup, and both of them with the rows quantized between: captured and replayed
+    beside the same calls on another stream, int8 rows too."""
+    g = torch.Generator("cuda").manual_seed(T + ff)
+    L = Layer(fp, g, E, d, ff, True)
+    sets = []
+    for i in range(3):
+        X = tokens(g, T, d, torch.bfloat16)
+        sets.append((X,) + route(g, T, K, E, drop=0.1 * i) + fp.quantize_rows(X))
+
+    def both(X, ids, w, q, s):
+        return L(fp, X, ids, w), L(fp, q, ids, w, x_scale=s)
+    want = [both(*s) for s in sets]
+    for (X, ids, w, q, s), (a, b) in zip(sets, want):
+        L.check(a, q, s, ids, w)
+        assert torch.equal(a, b)
+    args = [t.clone() for t in sets[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(*args)
+    for i in (1, 2, 0, 2, 1):
+        for a, b in zip(args, sets[i]):
+            a.copy_(b)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = both(*sets[(i + 1) % 3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+        assert all(torch.equal(a, b) for a, b in zip(other, want[(i + 1) % 3]))
+
+
+def test_values_that_leave_fp32(fp):
+    """A row of huge values: with a gate the hidden values leave fp32, which makes the token's output NaN; without one they do
+    not, and the output is as exact as any."""
+    g = torch.Generator("cuda").manual_seed(23)
+    for gate in (True, False):
+        L = Layer(fp, g, 4, 128, 64, gate)
+        X = tokens(g, 12, 128, torch.float32)
+        X[6] = 1e30
+        ids, w = route(g, 12, 2, 4)
+        q, s = fp.quantize_rows(X)
+        Y = L(fp, X, ids, w)
+        if gate:
+            assert bool(Y[6].isnan().all())
+            X[6] = 0
+            q, s = fp.quantize_rows(X)
+            Y[6] = L(fp, X, ids, w)[6]
+        L.check(Y, q, s, ids, w)
