@@ -397,7 +397,10 @@ size_t fp_token_logprobs_workspace(fp_dtype dt, int32_t T, int32_t V, int32_t to
  *   dX[t, v] = (dlogprob (1[v = token] - p_v) - dentropy p_v (log p_v + entropy))
  *              / temperature
  * in fp32, rounded once. A token outside [0, V) has no log probability and passes
- * no gradient of it; a row without any token gets zeros. dX [T, V] (lddx) may be X, with
+ * no gradient of it; a row without any token gets zeros, one with a NaN or
+ * +infinity NaN throughout. p_v is within about (6 |r| + 2) 2^-24 of itself at r =
+ * z_v - max z, and 0 below 2^-126: far tokens' gradients are less exact relative to
+ * themselves than those near the maximum. dX [T, V] (lddx) may be X, with
  * the same leading dimension. */
 int fp_token_logprobs_backward(fp_dtype dt, const void* X, int64_t ldx, int32_t T, int32_t V, const void* tokens,
                                int32_t id_bytes, float temperature, const float* dlogprob, const float* dentropy,

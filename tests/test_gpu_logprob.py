@@ -315,3 +315,25 @@ def test_streams_and_graphs(fp, T):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
         assert all(torch.equal(a, b) for a, b in zip(other, want[(i + 1) % 4]))
+
+
+@pytest.mark.parametrize("T,V", [(4, 700), (4, 40000), (520, 40000)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradient_of_bad_rows(fp, T, V, dtype):
+    """A row with a NaN or +infinity has a gradient of NaN throughout, whichever gradients come in and whatever its token; the
+    rows beside it keep theirs."""
+    g = torch.Generator("cuda").manual_seed(V)
+    X = logits(g, T, V, dtype)
+    d = torch.randn(T, generator=g, device="cuda")
+    tokens = torch.randint(0, V, (T,), generator=g, device="cuda")
+    rest = [0] + list(range(4, T))
+    clean = fp.token_logprobs(X, tokens)
+    X[1, V // 2], X[2, 0], X[3, V - 1] = math.nan, math.inf, math.nan
+    X[3, :V - 1] = -math.inf
+    for token in (4, V // 2, -1):
+        tokens[1:4] = token
+        lp = fp.token_logprobs(X, tokens)
+        for a, b in ((d, d), (d, None), (None, d), (None, None)):
+            dx = fp.token_logprobs_backward(a, b, X, tokens, lp)
+            assert bool(dx[1:4].isnan().all())
+            assert torch.equal(dx[rest], fp.token_logprobs_backward(a, b, torch.where(X.isfinite(), X, 0), tokens, clean)[rest])

@@ -1232,7 +1232,8 @@ def token_logprobs(logits, tokens, temperature: float = 1.0, top: int = 0, out: 
 
 def token_logprobs_backward(dlogprob, dentropy, logits, tokens, lp: TokenLogprobs, temperature: float = 1.0, out=None):
     """dlogits [T, V] in the logits' type, from the gradients of lp.logprob and lp.entropy (float32 [T]; None: zero), lp
-    being what token_logprobs said of the same logits, tokens and temperature. ``out`` may be the logits themselves."""
+    being what token_logprobs said of the same logits, tokens and temperature. ``out`` may be the logits themselves.
+    A row with a NaN or +infinity has a gradient of NaN throughout."""
     T, V, dt, ldx = _logit_args(logits, tokens)
     for g, name in ((dlogprob, "dlogprob"), (dentropy, "dentropy")):
         if g is not None:

@@ -437,6 +437,7 @@ __global__ __launch_bounds__(NT) void logprob_backward_kernel(LogBwdArgs a) {
       float d[EV];
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
+        // (of a row with a NaN or +infinity h is NaN, and with it every product)
         const float lp = fmaxf((load_elem<E>(raw[v], e) - m) * a.inv_t - log_s, -1e30f);
         const float p = __builtin_amdgcn_exp2f(lp * LOG2E);
         d[e] = dl * ((at + e == tok ? 1.f : 0.f) - p) - dh * p * (lp + h);
