@@ -321,3 +321,27 @@ def test_gradients_far_from_one(fp, size_h, size_g, eps, d, dtype):
     dx, dw = fp.rms_norm_backward(dY, H, w, eps=eps)
     assert torch.equal(dx[[0, 2]], plain[[0, 2]])
     check_gradients(dx, dw, dY, H, w, eps, None)
+
+
+@pytest.mark.parametrize("T,d", [(9000, 300), (2100, 1500), (512, 5000), (513, 5000), (2100, 5000), (513, 2100), (600, 9001), (1100, 20000)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_more_rows_than_workgroups(fp, T, d, dtype):
+    """Every form for many rows, each workgroup with several of them, bad ones between: floats, stream and int8 rows."""
+    g = torch.Generator("cuda").manual_seed(T + d)
+    X, R = rows(g, T, d, dtype), rows(g, T, d, dtype)
+    X[5::97, d // 3] = float("nan")
+    if dtype != torch.float16:
+        X[6::97] = 1e30
+        R[6::97] = 0
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(dtype)
+    Y = torch.empty_like(X)
+    q, scale, H = fp.rms_norm_quantize(X, w, residual=R, Y=Y)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[5::97] = True
+    assert bool(Y[bad].isnan().all()) and bool(scale[bad].isnan().all()) and bool((q[bad] == 0).all())
+    h, want = exact(X[~bad], w, 1e-5, R[~bad])
+    within(H[~bad], h, U * h.abs() + half_step(h, dtype))
+    within(Y[~bad], want, 60 * U * want.abs() + half_step(want, dtype))
+    step = scale[~bad].double()[:, None]
+    within(scale[~bad], want.abs().amax(1) / 127, 62 * U * want.abs().amax(1) / 127)
+    within(q[~bad].double() * step, want, (0.5 + 2.0 ** -14) * step + 61 * U * want.abs())

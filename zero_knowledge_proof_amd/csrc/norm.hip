@@ -448,8 +448,9 @@ void launch_norm_whole(const NormArgs& a, hipStream_t st) {
   if (vecs <= 32) rms_norm_kernel<E, W, 16, 2, WHOLE><<<grid(NT / 16), dim3(NT), 0, st>>>(a);
   else if (vecs <= 128) rms_norm_kernel<E, W, 64, 2, WHOLE><<<grid(NT / 64), dim3(NT), 0, st>>>(a);
   else if (vecs <= 512) rms_norm_kernel<E, W, 256, 2, WHOLE><<<grid(1), dim3(256), 0, st>>>(a);
-  // few rows, for the latency (one of 5120 bf16 with everything: 6.3 us, with 256 threads 7.0)
-  else if (vecs <= 1024 && a.T <= 64) rms_norm_kernel<E, W, 512, 2, WHOLE><<<grid(1), dim3(512), 0, st>>>(a);
+  // rows that are all under way at once, for the latency (5120 bf16 with everything, us:
+  // one row 6.2, with 256 threads 7.0; 64 6.6 and 7.4; 512 10.2 and 11.0; 4096 50 and 46)
+  else if (vecs <= 1024 && a.T <= 512) rms_norm_kernel<E, W, 512, 2, WHOLE><<<grid(1), dim3(512), 0, st>>>(a);
   else if (vecs <= 1024) rms_norm_kernel<E, W, 256, 4, WHOLE><<<grid(1), dim3(256), 0, st>>>(a);
   else rms_norm_kernel<E, W, 512, 4, WHOLE><<<dim3((unsigned)(a.T < 512 ? a.T : 512)), dim3(512), 0, st>>>(a);
 }
