@@ -455,7 +455,7 @@ __global__ __launch_bounds__(NT) void logprob_backward_kernel(LogBwdArgs a) {
   }
 }
 
-int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+using sdev::elem_bytes;
 
 struct Plan {
   int nv, splits, per;

@@ -387,7 +387,7 @@ __global__ __launch_bounds__(ROW_NT) void combine_backward_kernel(CombineBwdArgs
   }
 }
 
-int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+using sdev::elem_bytes;
 unsigned row_grid(int32_t T) { return (unsigned)(T < (1 << 20) ? T : 1 << 20); }
 
 int check_slots(const char* fn, int32_t T, int32_t K) {

@@ -625,7 +625,7 @@ __global__ __launch_bounds__(NT, wgs_of<XT>()) void moe_output_kernel(FewArgs a)
   }
 }
 
-int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+using sdev::elem_bytes;
 
 struct Scratch {
   size_t A, part, xs_out, top, xs, xq, as, aq, bytes;

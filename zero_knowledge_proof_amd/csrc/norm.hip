@@ -414,7 +414,7 @@ __global__ __launch_bounds__(NT) void rms_norm_dw_kernel(const float* part, int3
   }
 }
 
-int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+using sdev::elem_bytes;
 
 // Row types, width and eps, which the calls share.
 int check_norm(const char* fn, fp_dtype dt, fp_dtype w_dt, const void* w, float eps, int32_t T, int32_t d) {

@@ -645,7 +645,7 @@ int launch_scaled(const char* fn, const ScaledArgs& a, const GroupPtrs& gp, fp_d
   }
 }
 
-int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
+using sdev::elem_bytes;
 
 // What the product calls share: sizes, pointers, and how X may be read. T rows
 // are made from x_rows rows of X (if X has none, it and its scales may be NULL).

@@ -7,7 +7,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "fp.h"
+
 namespace sdev {
+
+// Bytes of a floating type's element; 0: it is none.
+inline int elem_bytes(fp_dtype dt) { return dt == FP_F32 ? 4 : (dt == FP_F16 || dt == FP_BF16 ? 2 : 0); }
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
