@@ -218,8 +218,8 @@ int fp_moe_combine_backward(fp_dtype dt, const void* dY, int64_t lddy, const voi
  * arrays of E device pointers to each expert's weights [ff, d] from
  * fp_witness_pack_weights, with gate_scale[e ld_gate + j] and up_scale likewise;
  * down: of [d, ff], with down_scale. Y [T, d] (ldy) in y_dt, which may be X; a token
- * without experts gets zeros. T K <= FP_MAX_FEW_SLOTS, E <= FP_MAX_EXPERTS, d and ff in
- * [1, FP_MAX_DIN]; sizes whose weights would be 2^43 bytes or more are refused
+ * without experts gets zeros, one with a hidden value that leaves fp32 NaN. T K <=
+ * FP_MAX_FEW_SLOTS, E <= FP_MAX_EXPERTS, d and ff in [1, FP_MAX_DIN]; sizes whose weights would be 2^43 bytes or more are refused
  * (FP_ESHAPE). ws: fp_moe_layer_workspace bytes, 256-byte aligned, contents
  * on entry do not matter. */
 int fp_moe_layer(fp_dtype x_dt, const void* X, int64_t ldx, const float* x_scale, const void* ids, int32_t id_bytes,
@@ -339,8 +339,9 @@ int fp_rms_norm(fp_dtype dt, const void* X, int64_t ldx, const void* R, int64_t 
                 float eps, int32_t T, int32_t d, void* H, int64_t ldh, void* Y, int64_t ldy, int8_t* Xq, int64_t ldq,
                 float* scale, hipStream_t stream);
 
-/* The norm's gradients at H [T, d] (what it normalized; X, or the sum that
- * fp_rms_norm left in H) from dY: with n = h / sqrt(mean(h^2) + eps),
+/* The norm's gradients at H [T, d] (X, or the sum that fp_rms_norm left in H, which
+ * in 16 bits is rounded, where the norm itself was of the sum before: the gradient is
+ * that of the norm of these rows) from dY: with n = h / sqrt(mean(h^2) + eps),
  *   dX = (dY w - n mean(dY w n)) / sqrt(mean(h^2) + eps) + dH  (dH NULL: 0)
  *   dw[j] = sum_t dY[t, j] n[t, j]   (device fp32 [d], or NULL)
  * in fp32, summed in an order fixed by T, d and the type. dX is also the gradient

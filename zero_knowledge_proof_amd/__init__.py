@@ -858,9 +858,9 @@ def rms_norm_quantize(X, weight, eps: float = 1e-5, residual=None, residual_out=
 
 
 def rms_norm_backward(dY, H, weight, eps: float = 1e-5, dH=None, out=None, dw=None):
-    """(dX, dw), the gradients of rms_norm at H [T, d] (its X, or the sum it returned) from dY: dX [T, d] in H's type, of X
-    and of the residual alike, with ``dH``, the gradient of H's other uses, added; dw float32 [d] (None without weights).
-    d is at most 16384."""
+    """(dX, dw), the gradients of rms_norm at H [T, d] (its X, or the sum it returned, as that was rounded) from dY: dX [T, d]
+    in H's type, of X and of the residual alike, with ``dH``, the gradient of H's other uses, added; dw float32 [d] (None
+    without weights). d is at most 16384."""
     shape, dtype, dt, ldh, w_dt, w = _norm_args(H, weight, "H")
     T, d = shape
     lddy = _rows_like(dY, dtype, shape, "dY")
@@ -1134,8 +1134,9 @@ def moe_layer(X, ids, weights, up: PackedExperts, up_scale, down: PackedExperts,
     strung together from scaled_linear's products by expert and moe_combine. X [T, d]: float32, float16 or bfloat16, or int8
     with ``x_scale`` (rms_norm_quantize's rows). ids [T, K] (int32 or int64 on the device): an id outside [0, experts) is a
     slot without an expert; weights float32 [T, K]. up, gate: pack_experts of [E, ff, d], down: of [E, d, ff], each with
-    float32 scales [E, outputs]. Y is in ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: tensors
-    that require one are refused unless under torch.no_grad."""
+    float32 scales [E, outputs]. With many small experts the calls for many tokens are faster from about 64 tokens on. Y is in
+    ``out``'s type, ``dtype``, X's, or bfloat16 for int8 X. It has no gradient: tensors that require one are refused unless
+    under torch.no_grad."""
     for t in (X, weights, x_scale, up_scale, down_scale, gate_scale):
         if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise ValueError("a tensor requires a gradient, which this layer does not have: train through moe_dispatch and "

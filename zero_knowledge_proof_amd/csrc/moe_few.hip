@@ -649,8 +649,9 @@ Scratch scratch(int64_t T, int64_t N, int64_t d, int64_t ff) {
 }
 
 // Rows quantized where they are multiplied, eight of an expert at a time (more read
-// the weights again): no expert has more than eight of 8 tokens, each with its own
-// experts, and few experts do of 32 with two rows an expert on average (16 tokens, 4
+// the weights again): of 8 tokens no expert has more than eight, unless a token
+// names one several times (right, but its weights are read once for every eight
+// rows), and of 32 with two rows an expert on average few have (16 tokens, 4
 // of 64, 1024 -> 512 -> 1024: 30 us, quantized between 35; 32 tokens of 4 of 64, 2048
 // -> 1024 -> 2048: 96, so 102; with more rows, 61 tokens, 3 of 20: 90, so 54;
 // skewed, 32 tokens of 1 of 16, 4096 -> 4096 -> 4096: 156, so 148).

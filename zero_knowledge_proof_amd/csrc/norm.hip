@@ -284,8 +284,8 @@ constexpr float LIFT = 0x1p60f;
 // P threads to a row, FT values each; a row to a workgroup from 128 threads on. A
 // thread has the same columns in every row that its workgroup takes (a stride of
 // the grid apart), so the columns' dw stay in its registers; a workgroup's sums
-// go to a row of `part`. Bound by the rows' bytes (8192 x 4096 bf16 with dh: 51 us
-// and 4.7 for the sums of `part`, 4.8 TB/s; 1500 x 1111 fp32, rows at any address and
+// go to a row of `part`. Bound by the rows' bytes (8192 x 4096 bf16 with dh: 52-55
+// us and 5 for the sums of `part`, 4.7 TB/s; 1500 x 1111 fp32, rows at any address and
 // partly from the MALL, 11.5 and 5).
 template <typename E, typename W, int P, bool WHOLE>
 __global__ __launch_bounds__(P > 64 ? P : NT) void rms_norm_backward_kernel(NormBwdArgs a) {
